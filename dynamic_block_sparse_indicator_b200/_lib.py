@@ -50,6 +50,21 @@ class PrismParams(C.Structure):
                 ("fixed_shape", C.c_int32), ("top_k_frac", C.c_float), ("cut_ratio", C.c_float)]
 
 
+PRISM_PAIR_ADJACENT = 0
+PRISM_PAIR_HALVES = 1
+
+
+class PrismNormRopeParams(C.Structure):
+    _fields_ = [("N", C.c_int64), ("T", C.c_int32), ("H", C.c_int32), ("W", C.c_int32), ("heads", C.c_int32),
+                ("head_dim", C.c_int32), ("dtype", C.c_int32), ("out_dtype", C.c_int32), ("w_dtype", C.c_int32),
+                ("dim_t", C.c_int32), ("dim_h", C.c_int32), ("dim_w", C.c_int32), ("pairing", C.c_int32),
+                ("eps", C.c_float)]
+
+
+class PrismRows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("head_stride", C.c_int64), ("token_stride", C.c_int64)]
+
+
 class PrismError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -103,6 +118,13 @@ def load(path: str | None = None) -> C.CDLL:
         "prism_zone_shapes_noalloc": (i32, [pp, vp, vp, vp, vp, vp]),
         "prism_av_norm": (i32, [C.c_int64, C.c_int32, C.c_int32, C.c_int32, vp, vp, vp, vp, vp,
                                 C.c_int32, vp, vp]),
+        "prism_rope_table": (i32, [C.POINTER(PrismNormRopeParams), C.c_float, C.c_int64, vp, vp]),
+        "prism_qk_norm_rope": (i32, [C.POINTER(PrismNormRopeParams), C.POINTER(PrismRows), C.POINTER(PrismRows), vp, vp,
+                                     vp, C.POINTER(PrismRows), C.POINTER(PrismRows), vp]),
+        "prism_qk_norm_rope_bwd_workspace_bytes": (sz, [C.POINTER(PrismNormRopeParams)]),
+        "prism_qk_norm_rope_bwd": (i32, [C.POINTER(PrismNormRopeParams), C.POINTER(PrismRows), C.POINTER(PrismRows),
+                                         C.POINTER(PrismRows), C.POINTER(PrismRows), vp, vp, vp, C.POINTER(PrismRows),
+                                         C.POINTER(PrismRows), vp, vp, vp, sz, vp]),
         "prism_status_read": (i32, [vp, C.POINTER(C.c_int32), vp]),
     }
     for name, (res, args) in sig.items():
@@ -491,3 +513,202 @@ def status_read(status, stream=None):
     site = C.c_int32(0)
     st = load().prism_status_read(_ptr(status), C.byref(site), _stream(stream))
     return int(st), int(site.value)
+
+
+# ---- the layer's operators around the attention -----------------------------------------
+
+def _code(dtype, what):
+    """PRISM_BF16 / PRISM_F32 of a torch dtype."""
+    import torch
+    if dtype == torch.bfloat16:
+        return PRISM_BF16
+    if dtype == torch.float32:
+        return PRISM_F32
+    raise ValueError(f"{what} must be bfloat16 or float32, got {dtype}")
+
+
+class _Launch:
+    """The device and stream of a call.  Makes the tensors' device current, and, where the
+    call runs on another stream than torch's current one, tells the caching allocator that
+    the tensors are in use there (their memory is not handed out again before it is done)."""
+
+    def __init__(self, tensors, stream):
+        import torch
+        self.tensors = [t for t in tensors if t is not None]
+        dev = self.tensors[0].device
+        if any(not t.is_cuda or t.device != dev for t in self.tensors):
+            raise ValueError("the tensors must be on one CUDA device")
+        self.guard = torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else None
+        cur = torch.cuda.current_stream(dev)
+        self.s = cur if stream is None else stream
+        if self.s.device != dev:
+            raise ValueError(f"the stream is on {self.s.device}, the tensors are on {dev}")
+        self.other = self.s.cuda_stream != cur.cuda_stream
+        self.stream = C.c_void_p(self.s.cuda_stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+    def empty(self, shape, dtype):
+        """Memory for the call (from torch's current stream, as every torch.empty)."""
+        import torch
+        t = torch.empty(shape, dtype=dtype, device=self.tensors[0].device)
+        self.tensors.append(t)
+        return t
+
+    def check(self, status, what):
+        if status:
+            raise PrismError(status, what)
+        if self.other:
+            for t in self.tensors:
+                t.record_stream(self.s)
+
+
+class Rope:
+    """A rotation table on the device with the grid and channels it belongs to (make_rope)."""
+
+    def __init__(self, table, T, H, W, dims, pairing):
+        self.table, self.T, self.H, self.W, self.dims, self.pairing = table, T, H, W, tuple(dims), pairing
+
+
+def _norm_rope_params(N, heads, D, dtype, out_dtype, w_dtype, rope, eps):
+    r = (rope.T, rope.H, rope.W, *rope.dims, rope.pairing) if rope is not None else (0, 0, 0, 0, 0, 0, 0)
+    return PrismNormRopeParams(N, r[0], r[1], r[2], heads, D, dtype, out_dtype, w_dtype, r[3], r[4], r[5], r[6],
+                               float(eps))
+
+
+def make_rope(T, H, W, dims, theta=10000.0, pairing=PRISM_PAIR_ADJACENT, first_frame=0, device=None, stream=None) -> Rope:
+    """The rotation of a T x H x W grid whose axes turn dims = (dim_t, dim_h, dim_w) channels
+    of each head (made once per grid; a 1-D sequence is (N, 1, 1) with dims (d, 0, 0))."""
+    import torch
+    dims = tuple(int(d) for d in dims)
+    if len(dims) != 3 or any(d < 0 or d % 2 for d in dims) or min(T, H, W) < 1:
+        raise ValueError(f"dims must be three even counts of channels and T, H, W positive, got {dims} and {(T, H, W)}")
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    table = torch.empty(max(T * dims[0] + H * dims[1] + W * dims[2], 4), dtype=torch.float32, device=dev)
+    rope = Rope(table, int(T), int(H), int(W), dims, int(pairing))
+    D = 64 if sum(dims) <= 64 else 128
+    p = _norm_rope_params(T * H * W, 1, D, PRISM_BF16, PRISM_BF16, PRISM_F32, rope, 1.0)
+    with _Launch([table], stream) as go:
+        go.check(load().prism_rope_table(C.byref(p), float(theta), int(first_frame), _ptr(table), go.stream),
+                 "prism_rope_table")
+    return rope
+
+
+def _rows(t, what):
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what} must be [heads, N, D] with consecutive channels (any head and token strides)")
+    return PrismRows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _weights(ws, D, what):
+    ws = [w for w in ws if w is not None]
+    for w in ws:
+        if tuple(w.shape) != (D,) or not w.is_contiguous() or w.dtype != ws[0].dtype:
+            raise ValueError(f"{what} must be contiguous vectors of the {D} channels, of one type")
+    return _code(ws[0].dtype, what) if ws else PRISM_F32
+
+
+def _qk_pair(named, rope):
+    """Checks a list of (name, query side, key side); returns heads, N, D."""
+    shape = tuple(named[0][1].shape)
+    if len(shape) != 3:
+        raise ValueError("q must be [heads, N, D]")
+    for name, a, b in named:
+        for t in (a, b):
+            if t is not None and tuple(t.shape) != shape:
+                raise ValueError(f"{name}: expected [heads, N, D] = {shape}, got {tuple(t.shape)}")
+        if (b is None) != (named[0][2] is None):
+            raise ValueError("the key's tensors must all be given or none")
+        if b is not None and b.dtype != a.dtype:
+            raise ValueError(f"{name}: query and key must be of one type")
+    heads, N, D = shape
+    if rope is not None and rope.T * rope.H * rope.W != N:
+        raise ValueError(f"the rotation is for {rope.T} x {rope.H} x {rope.W} tokens, q has {N}")
+    return heads, N, D
+
+
+def qk_norm_rope(q, k=None, wq=None, wk=None, rope=None, eps=1e-6, q_out=None, k_out=None, out_dtype=None, stream=None):
+    """(q_out, k_out): every head's rows of q and k [heads, N, D] scaled to unit root mean square,
+    multiplied by the weights [D] and rotated by `rope` (make_rope), each where given.  q and k are
+    bf16 or fp32 CUDA tensors of any head and token strides (slices of a fused projection); the
+    results are contiguous [heads, N, D] of out_dtype (q's type if not given), as `plan` takes them,
+    or the q_out, k_out given (of any strides; a result may be its own input)."""
+    import torch
+    out_dtype = out_dtype or (q_out.dtype if q_out is not None else q.dtype)
+    named = [("q, k", q, k)]
+    if q_out is None:
+        if k_out is not None:
+            raise ValueError("k_out without q_out")
+    else:
+        named.append(("q_out, k_out", q_out, k_out))
+        if q_out.dtype != out_dtype:
+            raise ValueError(f"q_out is {q_out.dtype}, out_dtype is {out_dtype}")
+    heads, N, D = _qk_pair(named, rope)
+    if wk is not None and k is None:
+        raise ValueError("wk without k")
+    dt, odt, wdt = _code(q.dtype, "q"), _code(out_dtype, "the result"), _weights((wq, wk), D, "wq and wk")
+    with _Launch([q, k, wq, wk, q_out, k_out, rope.table if rope is not None else None], stream) as go:
+        if q_out is None:
+            q_out = go.empty(q.shape, out_dtype)
+            k_out = go.empty(k.shape, out_dtype) if k is not None else None
+        p = _norm_rope_params(N, heads, D, dt, odt, wdt, rope, eps)
+        kr = None if k is None else C.byref(_rows(k, "k"))
+        kor = None if k is None else C.byref(_rows(k_out, "k_out"))
+        go.check(load().prism_qk_norm_rope(C.byref(p), C.byref(_rows(q, "q")), kr, _ptr(wq), _ptr(wk),
+                                           _ptr(rope.table) if rope is not None else None,
+                                           C.byref(_rows(q_out, "q_out")), kor, go.stream), "prism_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k=None, wq=None, wk=None, rope=None, eps=1e-6, dq=None, dk=None,
+                     want_dw=True, workspace=None, stream=None):
+    """(dq, dk, dwq, dwk): the gradients of qk_norm_rope by q, k (of their types, token-major as q is if q
+    is, or the dq, dk given) and by the weights (fp32 [D] for each weight given), from the gradients
+    dq_out, dk_out by its results and its own inputs."""
+    import torch
+    named = [("q, k", q, k), ("dq_out, dk_out", dq_out, dk_out)]
+    if dq is None:
+        if dk is not None:
+            raise ValueError("dk without dq")
+    else:
+        named.append(("dq, dk", dq, dk))
+        if dq.dtype != q.dtype:
+            raise ValueError(f"dq is {dq.dtype}, q is {q.dtype}")
+    heads, N, D = _qk_pair(named, rope)
+    if wk is not None and k is None:
+        raise ValueError("wk without k")
+    dt, gdt, wdt = _code(q.dtype, "q"), _code(dq_out.dtype, "dq_out"), _weights((wq, wk), D, "wq and wk")
+    with _Launch([q, k, dq_out, dk_out, wq, wk, dq, dk, workspace, rope.table if rope is not None else None],
+                 stream) as go:
+        def like(x):
+            """Dense, in the order of x's strides: token-major rows stay token-major."""
+            if x is None:
+                return None
+            if x.stride(1) > x.stride(0):
+                return go.empty((N, heads, D), x.dtype).transpose(0, 1)
+            return go.empty((heads, N, D), x.dtype)
+
+        if dq is None:
+            dq, dk = like(q), like(k)
+        dwq = go.empty((D,), torch.float32) if want_dw and wq is not None else None
+        dwk = go.empty((D,), torch.float32) if want_dw and wk is not None else None
+        p = _norm_rope_params(N, heads, D, dt, gdt, wdt, rope, eps)
+        lib = load()
+        if workspace is None and (dwq is not None or dwk is not None):
+            workspace = go.empty((max(int(lib.prism_qk_norm_rope_bwd_workspace_bytes(C.byref(p))), 16),), torch.uint8)
+        one = lambda t, what: None if t is None else C.byref(_rows(t, what))
+        go.check(lib.prism_qk_norm_rope_bwd(C.byref(p), one(dq_out, "dq_out"), one(dk_out, "dk_out"), one(q, "q"),
+                                            one(k, "k"), _ptr(wq), _ptr(wk),
+                                            _ptr(rope.table) if rope is not None else None, one(dq, "dq"),
+                                            one(dk, "dk"), _ptr(dwq), _ptr(dwk), _ptr(workspace),
+                                            workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                            go.stream), "prism_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk

@@ -1,0 +1,630 @@
+// prism_norm_rope.cu -- RMS norm of every head's query and key rows with the
+// rotation by grid position in the same pass, and its gradients.
+//
+// Row x (one token of one head, D channels), weight w, pair (a, b) of channels
+// turned by the angle of the token's position on the pair's axis (cos c, sin s):
+//     r = 1 / sqrt(mean_d x_d^2 + eps),  u = x r w,
+//     y_a = u_a c - u_b s,  y_b = u_a s + u_b c.
+// Gradients, with g = dy and v = R^T g (v_a = g_a c + g_b s, v_b = g_b c - g_a s):
+//     dw = sum over rows of v x r,   dx = r (w v - x r mean_d(w v x r)).
+//
+// Bound: HBM.  The forward moves each element twice (one read, one write), the
+// backward three times; the arithmetic is a few operations per element.  Nothing
+// but the inputs is kept for the backward: x has to be read again anyway, and r
+// follows from it.
+//
+// Layout: a row is D / 8 lanes of 8 channels (16-byte accesses for bf16), a warp
+// holds 32 / (D / 8) consecutive tokens of one head, and a block walks heads with
+// its tokens fixed, so a lane's cos and sin are read once for all the heads of its
+// token (they are gathered from three small per-axis tables: [T], [H], [W] rows
+// instead of one table of T H W rows).  Consecutive tokens of one head make the
+// head-major side of the pass contiguous; on a token-major side each row is still
+// whole 128-byte lines, and the following heads of the loop continue them.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "prism_dev.cuh"
+#include "prism_internal.h"
+
+namespace prism {
+namespace nr {
+
+constexpr int kThreads = 256;
+
+struct Rows {
+    void* p;
+    int64_t hs, ts;          // head and token strides in elements
+};
+
+struct Rope {
+    const float2* tab;       // (cos, sin): [T][dt/2], [H][dh/2], [W][dw/2]; null = no rotation
+    int T, H, W;
+    int dt, dh, dw;
+};
+
+struct Args {
+    Rows in[2], out[2], grad[2];   // forward: in -> out; backward: in = x, grad = dy, out = dx
+    const void* w[2];
+    int w_f32;
+    Rope rope;
+    int64_t N;
+    int heads, hpc;                // heads, heads per block
+    float eps;
+    float* part;                   // backward: [2][blocks of a tensor][D] partial weight gradients, or null
+};
+
+// ---------------------------------------------------------- 8-channel accesses
+template <typename T> struct Vec8;
+template <> struct Vec8<__nv_bfloat16> {
+    uint4 r;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void get(float* f) const {
+        const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                                       pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
+    }
+};
+template <> struct Vec8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float* f) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    static __device__ __forceinline__ void store(float* p, const float* f) {
+        __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+        __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+    }
+};
+
+// Sum over the LANES lanes that hold one row.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v) {
+    #pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ void load_w(const void* w, int f32, int ch, float* out) {
+    #pragma unroll
+    for (int i = 0; i < 8; ++i)
+        out[i] = !w ? 1.f : f32 ? static_cast<const float*>(w)[ch + i]
+                                : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[ch + i]);
+}
+
+// A lane's part of the rotation at one token.  Adjacent pairs (2p, 2p + 1) lie in one
+// lane: four (cos, sin).  With halves, channel p of an axis of d channels pairs with
+// p + d / 2, in general in another lane at no alignment (d / 2 may be odd), so the row
+// passes through shared memory and the lane keeps its eight channels' cos, sin (the
+// sign of the channel's own side folded in) and partners.  Channels behind the last
+// axis are not rotated: cos 1, sin 0.
+template <bool HALVES> struct Turn;
+
+__device__ __forceinline__ float2 rope_at(const Rope& r, int pair, int t, int h, int w) {
+    const int pt = r.dt >> 1, ph = r.dh >> 1, pw = r.dw >> 1;
+    if (pair < pt) return __ldg(r.tab + (int64_t)t * pt + pair);
+    pair -= pt;
+    if (pair < ph) return __ldg(r.tab + (int64_t)r.T * pt + (int64_t)h * ph + pair);
+    pair -= ph;
+    if (pair < pw) return __ldg(r.tab + (int64_t)r.T * pt + (int64_t)r.H * ph + (int64_t)w * pw + pair);
+    return make_float2(1.f, 0.f);
+}
+
+template <> struct Turn<false> {
+    float2 cs[4];
+    __device__ __forceinline__ void init(const Rope& r, int ch, int t, int h, int w) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) cs[i] = rope_at(r, (ch >> 1) + i, t, h, w);
+    }
+    // u -> R u (DIR = 1) or R^T u (DIR = -1)
+    template <int DIR>
+    __device__ __forceinline__ void apply(float* u, float*, int) const {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = u[2 * i], b = u[2 * i + 1], c = cs[i].x, s = DIR * cs[i].y;
+            u[2 * i] = a * c - b * s;
+            u[2 * i + 1] = a * s + b * c;
+        }
+    }
+};
+
+template <> struct Turn<true> {
+    float c[8], s[8];
+    int at[8];               // the partners' places in the row's shared-memory copy
+    // one pad word per 8 channels: the lanes of a row write and read at an odd stride
+    static __device__ __forceinline__ int place(int ch) { return ch + (ch >> 3); }
+    __device__ __forceinline__ void init(const Rope& r, int ch, int t, int h, int w) {
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = ch + i;
+            int base = 0, d = r.dt;
+            if (e >= r.dt) { base = r.dt; d = r.dh; }
+            if (e >= r.dt + r.dh) { base = r.dt + r.dh; d = r.dw; }
+            const int l = e - base, half = d >> 1;
+            if (l >= d) {
+                c[i] = 1.f; s[i] = 0.f; at[i] = place(e);
+            } else {
+                const bool lo = l < half;
+                const float2 v = rope_at(r, (base >> 1) + (lo ? l : l - half), t, h, w);
+                c[i] = v.x;
+                s[i] = lo ? -v.y : v.y;
+                at[i] = place(lo ? e + half : e - half);
+            }
+        }
+    }
+    template <int DIR>
+    __device__ __forceinline__ void apply(float* u, float* row, int ch) const {
+        float* mine = row + place(ch);
+        __syncwarp();                        // the previous row's reads are done
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) mine[i] = u[i];
+        __syncwarp();
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = u[i] * c[i] + DIR * s[i] * row[at[i]];
+    }
+};
+
+// Rows of shared memory for the exchange (HALVES only): one row per row of the block.
+template <int D, bool HALVES>
+struct Exchange {
+    static constexpr int kRows = kThreads / (D / 8);
+    static constexpr int kPitch = D + D / 8;
+    static constexpr int kFloats = HALVES ? kRows * kPitch : 1;
+};
+
+// Grid: x = token tiles (strided), y = head groups, z = query or key.
+template <typename TI, typename TO, int D, bool HALVES>
+__global__ void __launch_bounds__(kThreads) k_norm_rope(const Args a) {
+    constexpr int LANES = D / 8, RPB = kThreads / LANES, U = 4;
+    __shared__ float sx[Exchange<D, HALVES>::kFloats];
+    const int z = blockIdx.z, ch = (threadIdx.x % LANES) * 8, sub = threadIdx.x / LANES;
+    float* row = HALVES ? sx + sub * Exchange<D, HALVES>::kPitch : nullptr;
+    const Rows in = a.in[z], out = a.out[z];
+    const int h0 = blockIdx.y * a.hpc, h1 = min(h0 + a.hpc, a.heads);
+    float w[8];
+    load_w(a.w[z], a.w_f32, ch, w);
+    for (int64_t n0 = (int64_t)blockIdx.x * RPB; n0 < a.N; n0 += (int64_t)gridDim.x * RPB) {
+        const int64_t n = n0 + sub;
+        const bool ok = n < a.N;
+        Turn<HALVES> turn;
+        if (a.rope.tab) {
+            const int64_t m = ok ? n : 0, hw = (int64_t)a.rope.H * a.rope.W;
+            const int t = (int)(m / hw), r = (int)(m - t * hw);
+            turn.init(a.rope, ch, t, r / a.rope.W, r % a.rope.W);
+        }
+        const TI* src = static_cast<const TI*>(in.p) + n * in.ts + ch;
+        TO* dst = static_cast<TO*>(out.p) + n * out.ts + ch;
+        for (int h = h0; h < h1; h += U) {
+            Vec8<TI> v[U];
+            #pragma unroll
+            for (int i = 0; i < U; ++i) {
+                v[i] = Vec8<TI>{};
+                if (ok && h + i < h1) v[i].load(src + (h + i) * in.hs);
+            }
+            #pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (h + i >= h1) break;      // the same for the whole block
+                float x[8], ss = 0.f;
+                v[i].get(x);
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+                const float r = rsqrtf(row_sum<LANES>(ss) * (1.f / D) + a.eps);
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+                if (a.rope.tab) turn.template apply<1>(x, row, ch);
+                if (ok) Vec8<TO>::store(dst + (h + i) * out.hs, x);
+            }
+        }
+    }
+}
+
+// The gradients.  TI: type of x and dx; TG: type of dy.  A block sums its rows' part of
+// dw in registers (in the order of its loop), then over its rows through shared memory,
+// and writes one row of partial sums: no atomics, the same bits every time.
+template <typename TI, typename TG, int D, bool HALVES>
+__global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const Args a) {
+    constexpr int LANES = D / 8, RPB = kThreads / LANES, U = 2;
+    constexpr int kSum = RPB * D;
+    constexpr int kEx = Exchange<D, HALVES>::kFloats;
+    __shared__ float sx[kSum > kEx ? kSum : kEx];
+    const int z = blockIdx.z, ch = (threadIdx.x % LANES) * 8, sub = threadIdx.x / LANES;
+    float* row = HALVES ? sx + sub * Exchange<D, HALVES>::kPitch : nullptr;
+    const Rows in = a.in[z], out = a.out[z], grad = a.grad[z];
+    const int h0 = blockIdx.y * a.hpc, h1 = min(h0 + a.hpc, a.heads);
+    float w[8], dw[8];
+    load_w(a.w[z], a.w_f32, ch, w);
+    #pragma unroll
+    for (int e = 0; e < 8; ++e) dw[e] = 0.f;
+    for (int64_t n0 = (int64_t)blockIdx.x * RPB; n0 < a.N; n0 += (int64_t)gridDim.x * RPB) {
+        const int64_t n = n0 + sub;
+        const bool ok = n < a.N;
+        Turn<HALVES> turn;
+        if (a.rope.tab) {
+            const int64_t m = ok ? n : 0, hw = (int64_t)a.rope.H * a.rope.W;
+            const int t = (int)(m / hw), r = (int)(m - t * hw);
+            turn.init(a.rope, ch, t, r / a.rope.W, r % a.rope.W);
+        }
+        const TI* src = static_cast<const TI*>(in.p) + n * in.ts + ch;
+        const TG* gsr = static_cast<const TG*>(grad.p) + n * grad.ts + ch;
+        TI* dst = static_cast<TI*>(out.p) + n * out.ts + ch;
+        for (int h = h0; h < h1; h += U) {
+            Vec8<TI> v[U];
+            Vec8<TG> q[U];
+            #pragma unroll
+            for (int i = 0; i < U; ++i) {
+                v[i] = Vec8<TI>{};
+                q[i] = Vec8<TG>{};
+                if (ok && h + i < h1) {
+                    v[i].load(src + (h + i) * in.hs);
+                    q[i].load(gsr + (h + i) * grad.hs);
+                }
+            }
+            #pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (h + i >= h1) break;      // the same for the whole block
+                float x[8], g[8], ss = 0.f, dot = 0.f;
+                v[i].get(x);
+                q[i].get(g);
+                if (a.rope.tab) turn.template apply<-1>(g, row, ch);
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    ss = fmaf(x[e], x[e], ss);
+                    dot = fmaf(g[e] * w[e], x[e], dot);
+                }
+                ss = row_sum<LANES>(ss);
+                dot = row_sum<LANES>(dot);
+                const float r = rsqrtf(ss * (1.f / D) + a.eps);
+                const float k = dot * r * r * (1.f / D);
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    // a token behind the last one has x = g = 0 and adds nothing
+                    dw[e] = fmaf(g[e], x[e] * r, dw[e]);
+                    x[e] = r * (g[e] * w[e] - k * x[e]);
+                }
+                if (ok) Vec8<TI>::store(dst + (h + i) * out.hs, x);
+            }
+        }
+    }
+    if (a.part) {
+        __syncthreads();                     // the exchange rows are free
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) sx[sub * D + ch + e] = dw[e];
+        __syncthreads();
+        if (threadIdx.x < D) {
+            float s = 0.f;
+            for (int i = 0; i < RPB; ++i) s += sx[i * D + threadIdx.x];
+            const int64_t blk = ((int64_t)z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+            a.part[blk * D + threadIdx.x] = s;
+        }
+    }
+}
+
+// dw of tensor blockIdx.x: the `blocks` rows of partial sums in a fixed order, in 64 bits
+// (a sum over every token and head: its parts cancel).
+template <int D>
+__global__ void __launch_bounds__(1024) k_norm_rope_dw(const float* part, int blocks, float* dwq, float* dwk) {
+    constexpr int G = 1024 / D;
+    __shared__ double sm[1024];
+    const int c = threadIdx.x % D, g = threadIdx.x / D;
+    const float* p = part + (int64_t)blockIdx.x * blocks * D;
+    double s = 0.0;
+    for (int i = g; i < blocks; i += G) s += p[(int64_t)i * D + c];
+    sm[threadIdx.x] = s;
+    __syncthreads();
+    if (g == 0) {
+        for (int i = 1; i < G; ++i) s += sm[i * D + c];
+        float* dw = blockIdx.x ? dwk : dwq;
+        if (dw) dw[c] = (float)s;
+    }
+}
+
+// cos and sin of position * theta^(-2 p / d) in 64 bits, rounded once.
+__global__ void k_rope_table(int L, int d, int64_t first, double theta, float2* out) {
+    const int half = d >> 1, i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= L * half) return;
+    const int l = i / half, p = i - l * half;
+    double s, c;
+    sincos((double)(first + l) * pow(theta, -2.0 * p / d), &s, &c);
+    out[i] = make_float2((float)c, (float)s);
+}
+
+// ------------------------------------------------------------- host side
+static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+static int elt(int dtype) { return dtype == PRISM_F32 ? 4 : 2; }
+
+static bool bad_params(const prism_norm_rope_params* p) {
+    if (!p || p->N < 0 || p->N > 0x7fffffffLL || p->heads < 1 || p->heads > 65535 ||
+        (p->head_dim != 64 && p->head_dim != 128))
+        return true;
+    for (int d : {p->dtype, p->out_dtype, p->w_dtype})
+        if (d != PRISM_BF16 && d != PRISM_F32) return true;
+    return !(p->eps > 0.f) || !(p->eps < 3.0e38f);
+}
+
+static bool bad_rope(const prism_norm_rope_params* p) {
+    if (p->T < 1 || p->H < 1 || p->W < 1 || (int64_t)p->H * p->W > 0x7fffffffLL ||
+        (int64_t)p->T * ((int64_t)p->H * p->W) != p->N)
+        return true;
+    for (int d : {p->dim_t, p->dim_h, p->dim_w})
+        if (d < 0 || (d & 1) || d > p->head_dim) return true;
+    return p->dim_t + p->dim_h + p->dim_w > p->head_dim ||
+           (p->pairing != PRISM_PAIR_ADJACENT && p->pairing != PRISM_PAIR_HALVES);
+}
+
+// Rows must start on 16 bytes; a stride is free when its extent is one.
+static bool bad_rows(const prism_rows* r, int dtype, int64_t N, int heads) {
+    const int64_t q = 16 / elt(dtype);
+    return !r->data || !aligned16(r->data) || (heads > 1 && (r->head_stride % q || r->head_stride < 0)) ||
+           (N > 1 && (r->token_stride % q || r->token_stride < 0));
+}
+
+// The byte layout of a tensor of rows, for the check that what is written shares no
+// element with what else the call reads or writes.
+struct Span {
+    uintptr_t lo, hi;        // first and one past the last byte
+    int64_t hs, ts;          // strides in bytes (0 where the extent is one)
+    int heads;
+    int64_t N, row;          // row bytes
+};
+
+static Span span_of(const prism_rows* r, int dtype, int64_t N, int heads, int D) {
+    Span s;
+    const int e = elt(dtype);
+    s.hs = heads > 1 ? r->head_stride * e : 0;
+    s.ts = N > 1 ? r->token_stride * e : 0;
+    s.heads = heads;
+    s.N = N;
+    s.row = (int64_t)D * e;
+    s.lo = reinterpret_cast<uintptr_t>(r->data);
+    s.hi = s.lo + (uintptr_t)(s.hs * (heads - 1) + s.ts * (N - 1) + s.row);
+    return s;
+}
+
+// A tensor's rows do not overlap one another (else two rows would be written to one place).
+static bool rows_apart(const Span& s) {
+    const int64_t a = s.hs, b = s.ts;
+    if (s.heads > 1 && a < s.row) return false;
+    if (s.N > 1 && b < s.row) return false;
+    if (s.heads <= 1 || s.N <= 1) return true;
+    return a >= b ? a >= b * (s.N - 1) + s.row : b >= a * (s.heads - 1) + s.row;
+}
+
+// Whether two tensors certainly share no byte: apart as ranges, or of the same strides with
+// rows that fall between each other's (slices of one fused buffer).
+static bool apart(const Span& x, const Span& y) {
+    if (x.hi <= y.lo || y.hi <= x.lo) return true;
+    if (x.ts != y.ts || x.hs != y.hs || x.N != y.N || x.heads != y.heads) return false;
+    // the inner extent of one step of the outer stride
+    const bool tok_out = x.ts >= x.hs;
+    const int64_t outer = tok_out ? x.ts : x.hs;
+    const int64_t xin = (tok_out ? x.hs * (x.heads - 1) : x.ts * (x.N - 1)) + x.row;
+    const int64_t yin = (tok_out ? y.hs * (y.heads - 1) : y.ts * (y.N - 1)) + y.row;
+    if (outer <= 0) return false;
+    const uintptr_t d = y.lo >= x.lo ? y.lo - x.lo : x.lo - y.lo;
+    const int64_t m = (int64_t)(d % (uintptr_t)outer);
+    return y.lo >= x.lo ? m >= xin && outer - m >= yin : m >= yin && outer - m >= xin;
+}
+
+static bool same(const Span& x, const Span& y) {
+    return x.lo == y.lo && x.hs == y.hs && x.ts == y.ts && x.row == y.row;
+}
+
+static int device_ok() {
+    int dev = 0, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PRISM_ERR_UNSUPPORTED;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    return major == 10 && minor == 0 ? PRISM_OK : PRISM_ERR_UNSUPPORTED;
+}
+
+struct Grid {
+    int x, y, z, hpc;
+};
+
+// Blocks of a call.  One block takes every head of its tokens (its cos and sin are then
+// read once) unless that leaves fewer blocks than two per SM: then the heads are split.
+// The number of token tiles in flight is capped at 8 blocks per SM, the rest are walked.
+static Grid grid_of(int64_t N, int heads, int D, int z) {
+    const int64_t rpb = kThreads / (D / 8), tiles = (N + rpb - 1) / rpb;
+    Grid g;
+    g.z = z;
+    g.hpc = heads;
+    while (g.hpc > 1 && tiles * ((heads + g.hpc - 1) / g.hpc) * z < 2 * 148) g.hpc = (g.hpc + 1) / 2;
+    g.y = (heads + g.hpc - 1) / g.hpc;
+    const int64_t cap = 8 * 148 / ((int64_t)g.y * z) > 1 ? 8 * 148 / ((int64_t)g.y * z) : 1;
+    g.x = (int)(tiles < cap ? tiles : cap);
+    return g;
+}
+
+static Rope rope_of(const prism_norm_rope_params* p, const float* table) {
+    Rope r;
+    r.tab = reinterpret_cast<const float2*>(table);
+    r.T = p->T; r.H = p->H; r.W = p->W;
+    r.dt = p->dim_t; r.dh = p->dim_h; r.dw = p->dim_w;
+    return r;
+}
+
+template <typename TI, typename TO, bool BWD>
+static void launch(const Args& a, const Grid& g, int D, bool halves, cudaStream_t s) {
+    const dim3 grid(g.x, g.y, g.z);
+#define PRISM_NR(DD, HH)                                                        \
+    (BWD ? k_norm_rope_bwd<TI, TO, DD, HH><<<grid, kThreads, 0, s>>>(a)         \
+         : k_norm_rope<TI, TO, DD, HH><<<grid, kThreads, 0, s>>>(a))
+    if (D == 128) halves ? PRISM_NR(128, true) : PRISM_NR(128, false);
+    else halves ? PRISM_NR(64, true) : PRISM_NR(64, false);
+#undef PRISM_NR
+}
+
+template <bool BWD>
+static int dispatch(const prism_norm_rope_params* p, const Args& a, const Grid& g, cudaStream_t s) {
+    using bf = __nv_bfloat16;
+    const bool halves = a.rope.tab && p->pairing == PRISM_PAIR_HALVES;
+    if (p->dtype == PRISM_BF16)
+        p->out_dtype == PRISM_BF16 ? launch<bf, bf, BWD>(a, g, p->head_dim, halves, s)
+                                   : launch<bf, float, BWD>(a, g, p->head_dim, halves, s);
+    else
+        p->out_dtype == PRISM_BF16 ? launch<float, bf, BWD>(a, g, p->head_dim, halves, s)
+                                   : launch<float, float, BWD>(a, g, p->head_dim, halves, s);
+    return cudaGetLastError() == cudaSuccess ? PRISM_OK : PRISM_ERR_CUDA;
+}
+
+static Rows rows_of(const prism_rows* r) { return Rows{r->data, r->head_stride, r->token_stride}; }
+
+static int64_t part_rows(int64_t N, int heads, int D, int z) {
+    const Grid g = grid_of(N, heads, D, z);
+    return (int64_t)g.x * g.y * g.z;
+}
+
+}  // namespace nr
+}  // namespace prism
+
+extern "C" int prism_rope_table(const prism_norm_rope_params* p, float theta, int64_t first_frame, float* table,
+                                void* stream) {
+    using namespace prism::nr;
+    if (bad_params(p) || p->N < 1 || bad_rope(p) || !table || !aligned16(table) || !(theta > 0.f) || !(theta < 3.0e38f) ||
+        first_frame < 0 || first_frame > (1LL << 40))
+        return PRISM_ERR_INVALID_ARG;
+    if (int st = device_ok()) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    float2* out = reinterpret_cast<float2*>(table);
+    const int L[3] = {p->T, p->H, p->W}, d[3] = {p->dim_t, p->dim_h, p->dim_w};
+    for (int i = 0; i < 3; ++i) {
+        const int64_t n = (int64_t)L[i] * (d[i] / 2);
+        if (n > 0x7fffffffLL - 256) return PRISM_ERR_INVALID_ARG;
+        if (n == 0) continue;
+        k_rope_table<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(L[i], d[i], i == 0 ? first_frame : 0, (double)theta, out);
+        out += n;
+    }
+    return cudaGetLastError() == cudaSuccess ? PRISM_OK : PRISM_ERR_CUDA;
+}
+
+extern "C" int prism_qk_norm_rope(const prism_norm_rope_params* p, const prism_rows* q, const prism_rows* k,
+                                  const void* wq, const void* wk, const float* rope, const prism_rows* q_out,
+                                  const prism_rows* k_out, void* stream) {
+    using namespace prism::nr;
+    if (bad_params(p) || !q || !q_out || !k != !k_out) return PRISM_ERR_INVALID_ARG;
+    if (p->N == 0) return PRISM_OK;
+    if (rope && (!aligned16(rope) || bad_rope(p))) return PRISM_ERR_INVALID_ARG;
+    if (!aligned16(wq) || !aligned16(wk) || (wk && !k)) return PRISM_ERR_INVALID_ARG;
+    const int D = p->head_dim, z = k ? 2 : 1;
+    const prism_rows* in[2] = {q, k};
+    const prism_rows* out[2] = {q_out, k_out};
+    Span si[2], so[2];
+    for (int i = 0; i < z; ++i) {
+        if (bad_rows(in[i], p->dtype, p->N, p->heads) || bad_rows(out[i], p->out_dtype, p->N, p->heads))
+            return PRISM_ERR_INVALID_ARG;
+        si[i] = span_of(in[i], p->dtype, p->N, p->heads, D);
+        so[i] = span_of(out[i], p->out_dtype, p->N, p->heads, D);
+        if (!rows_apart(so[i])) return PRISM_ERR_INVALID_ARG;
+    }
+    for (int i = 0; i < z; ++i)
+        for (int j = 0; j < z; ++j)
+            if (!apart(so[i], si[j]) && !(i == j && same(so[i], si[j]))) return PRISM_ERR_INVALID_ARG;
+    if (z == 2 && !apart(so[0], so[1])) return PRISM_ERR_INVALID_ARG;
+    if (int st = device_ok()) return st;
+    Args a{};
+    for (int i = 0; i < z; ++i) {
+        a.in[i] = rows_of(in[i]);
+        a.out[i] = rows_of(out[i]);
+    }
+    a.w[0] = wq;
+    a.w[1] = wk;
+    a.w_f32 = p->w_dtype == PRISM_F32;
+    a.rope = rope_of(p, rope);
+    a.N = p->N;
+    a.heads = p->heads;
+    a.eps = p->eps;
+    const Grid g = grid_of(p->N, p->heads, D, z);
+    a.hpc = g.hpc;
+    nvtxRangePushA("prism qk norm rope");
+    const int st = dispatch<false>(p, a, g, static_cast<cudaStream_t>(stream));
+    nvtxRangePop();
+    return st;
+}
+
+extern "C" size_t prism_qk_norm_rope_bwd_workspace_bytes(const prism_norm_rope_params* p) {
+    using namespace prism::nr;
+    if (bad_params(p)) return 0;
+    if (p->N == 0) return 16;
+    const int64_t one = part_rows(p->N, p->heads, p->head_dim, 1), two = part_rows(p->N, p->heads, p->head_dim, 2);
+    return (size_t)(one > two ? one : two) * p->head_dim * sizeof(float);
+}
+
+extern "C" int prism_qk_norm_rope_bwd(const prism_norm_rope_params* p, const prism_rows* dq_out,
+                                      const prism_rows* dk_out, const prism_rows* q, const prism_rows* k,
+                                      const void* wq, const void* wk, const float* rope, const prism_rows* dq,
+                                      const prism_rows* dk, float* dwq, float* dwk, void* workspace, size_t ws_bytes,
+                                      void* stream) {
+    using namespace prism::nr;
+    if (bad_params(p) || !q || !dq_out || !dq || !k != !dk_out || !k != !dk) return PRISM_ERR_INVALID_ARG;
+    if ((dwk || wk) && !k) return PRISM_ERR_INVALID_ARG;
+    if (!aligned16(wq) || !aligned16(wk) || !aligned16(dwq) || !aligned16(dwk)) return PRISM_ERR_INVALID_ARG;
+    if (dwq && dwq == dwk) return PRISM_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int D = p->head_dim, z = k ? 2 : 1;
+    if (p->N == 0) {         // no rows: the weights' gradients are zero
+        for (float* dw : {dwq, dwk})
+            if (dw && cudaMemsetAsync(dw, 0, D * sizeof(float), s) != cudaSuccess) return PRISM_ERR_CUDA;
+        return PRISM_OK;
+    }
+    if (rope && (!aligned16(rope) || bad_rope(p))) return PRISM_ERR_INVALID_ARG;
+    const prism_rows* in[2] = {q, k};
+    const prism_rows* gr[2] = {dq_out, dk_out};
+    const prism_rows* out[2] = {dq, dk};
+    Span si[2], sg[2], so[2];
+    for (int i = 0; i < z; ++i) {
+        if (bad_rows(in[i], p->dtype, p->N, p->heads) || bad_rows(gr[i], p->out_dtype, p->N, p->heads) ||
+            bad_rows(out[i], p->dtype, p->N, p->heads))
+            return PRISM_ERR_INVALID_ARG;
+        si[i] = span_of(in[i], p->dtype, p->N, p->heads, D);
+        sg[i] = span_of(gr[i], p->out_dtype, p->N, p->heads, D);
+        so[i] = span_of(out[i], p->dtype, p->N, p->heads, D);
+        if (!rows_apart(so[i])) return PRISM_ERR_INVALID_ARG;
+    }
+    for (int i = 0; i < z; ++i)
+        for (int j = 0; j < z; ++j) {
+            if (!apart(so[i], si[j]) && !(i == j && same(so[i], si[j]))) return PRISM_ERR_INVALID_ARG;
+            if (!apart(so[i], sg[j]) && !(i == j && same(so[i], sg[j]))) return PRISM_ERR_INVALID_ARG;
+        }
+    if (z == 2 && !apart(so[0], so[1])) return PRISM_ERR_INVALID_ARG;
+    const bool want = dwq || dwk;
+    if (want && (!workspace || !aligned16(workspace))) return PRISM_ERR_INVALID_ARG;
+    if (want && ws_bytes < prism_qk_norm_rope_bwd_workspace_bytes(p)) return PRISM_ERR_WORKSPACE;
+    if (int st = device_ok()) return st;
+    Args a{};
+    for (int i = 0; i < z; ++i) {
+        a.in[i] = rows_of(in[i]);
+        a.grad[i] = rows_of(gr[i]);
+        a.out[i] = rows_of(out[i]);
+    }
+    a.w[0] = wq;
+    a.w[1] = wk;
+    a.w_f32 = p->w_dtype == PRISM_F32;
+    a.rope = rope_of(p, rope);
+    a.N = p->N;
+    a.heads = p->heads;
+    a.eps = p->eps;
+    const Grid g = grid_of(p->N, p->heads, D, z);
+    a.hpc = g.hpc;
+    a.part = want ? static_cast<float*>(workspace) : nullptr;
+    nvtxRangePushA("prism qk norm rope bwd");
+    int st = dispatch<true>(p, a, g, s);
+    if (!st && want) {
+        if (D == 128) k_norm_rope_dw<128><<<z, 1024, 0, s>>>(a.part, g.x * g.y, dwq, dwk);
+        else k_norm_rope_dw<64><<<z, 1024, 0, s>>>(a.part, g.x * g.y, dwq, dwk);
+        if (cudaGetLastError() != cudaSuccess) st = PRISM_ERR_CUDA;
+    }
+    nvtxRangePop();
+    return st;
+}

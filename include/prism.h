@@ -392,6 +392,98 @@ PRISM_API int prism_av_norm(int64_t N, int32_t M, int32_t heads, int32_t head_di
  * receives the site of a timed-out wait. */
 PRISM_API int prism_status_read(int32_t* dev_status, int32_t* site, void* stream);
 
+/* ---- query and key norm with rotation ------------------------------------ */
+/*
+ * prism_qk_norm_rope -- what makes prism_plan's Q and K from the projection's
+ *   output: every head's row x of D channels is scaled to unit root mean
+ *   square, multiplied by a weight and rotated by the token's grid position,
+ *     u = x w / sqrt(mean_d x_d^2 + eps),
+ *     y_a = u_a cos - u_b sin,  y_b = u_a sin + u_b cos  for each pair (a, b),
+ *   in one pass (fp32 arithmetic, one rounding to out_dtype).
+ * prism_norm_rope_params
+ *   N          tokens, 0 .. 2^31 - 1 (0: the call does nothing).
+ *   T, H, W    the grid, T H W = N, token n = (t H + h) W + w; any positive
+ *              sizes (a 1-D sequence is N x 1 x 1).  Read only with a rotation.
+ *   heads      1 .. 65535;  head_dim D, 64 or 128.
+ *   dtype      element type of q, k (and of their gradients);
+ *   out_dtype  of the results (and of the gradients by them);
+ *   w_dtype    of the weights: PRISM_BF16 or PRISM_F32 each.
+ *   dim_t, dim_h, dim_w   channels that each axis rotates: even, >= 0, at most
+ *              D together.  The axes take consecutive channels in this order;
+ *              the channels behind them are not rotated.
+ *   pairing    which channels of an axis of d channels form pair p:
+ *              PRISM_PAIR_ADJACENT 2p and 2p + 1, PRISM_PAIR_HALVES p and
+ *              p + d / 2.
+ *   eps        > 0 and finite.
+ * Arguments
+ *   q, k       host structs: the rows' device address and strides in elements
+ *              (row (h, n) at data + h head_stride + n token_stride, D
+ *              consecutive elements), so a slice of a fused [N][3][heads][D]
+ *              buffer is read in place.  Addresses 16-byte aligned, strides
+ *              whole multiples of 16 bytes, >= 0 (a stride is not read where
+ *              its extent is one).  k NULL: q alone.
+ *   wq, wk     device, D weights of w_dtype shared by the heads, or NULL (ones).
+ *   rope       device, the rotation table, or NULL (no rotation): fp32 pairs
+ *              (cos, sin), [T][dim_t / 2] then [H][dim_h / 2] then
+ *              [W][dim_w / 2], for instance from prism_rope_table.
+ *   q_out, k_out   the results' rows; [heads][N][D] with head_stride N D and
+ *              token_stride D is what prism_plan reads.  A result may be its own
+ *              input (same address, strides and element size); any other
+ *              overlap of what is written is refused (PRISM_ERR_INVALID_ARG).
+ *              Nothing outside the rows is written.
+ * prism_rope_table writes that table: angle position theta^(-2 p / d) for pair p
+ *   of an axis of d channels, the T axis starting at first_frame (a sequence
+ *   shard's offset), computed in 64 bits.
+ */
+#define PRISM_PAIR_ADJACENT 0
+#define PRISM_PAIR_HALVES   1
+typedef struct prism_norm_rope_params {
+    int64_t N;
+    int32_t T, H, W;
+    int32_t heads;
+    int32_t head_dim;
+    int32_t dtype;
+    int32_t out_dtype;
+    int32_t w_dtype;
+    int32_t dim_t, dim_h, dim_w;
+    int32_t pairing;
+    float   eps;
+} prism_norm_rope_params;
+
+typedef struct prism_rows {
+    void*   data;
+    int64_t head_stride;
+    int64_t token_stride;
+} prism_rows;
+
+PRISM_API int prism_rope_table(const prism_norm_rope_params* p, float theta, int64_t first_frame, float* table,
+                               void* stream);
+PRISM_API int prism_qk_norm_rope(const prism_norm_rope_params* p, const prism_rows* q, const prism_rows* k,
+                                 const void* wq, const void* wk, const float* rope, const prism_rows* q_out,
+                                 const prism_rows* k_out, void* stream);
+
+/*
+ * prism_qk_norm_rope_bwd -- its gradients, from the same inputs (nothing is kept
+ *   by the forward):
+ *   dq_out, dk_out   gradients by the results (out_dtype rows: what
+ *                    prism_attn_bwd writes as dQ, dK);
+ *   dq, dk           gradients by q, k (dtype rows, written); each may be its own
+ *                    dq_out / dk_out or q / k in place, else nothing may overlap;
+ *   dwq, dwk         device fp32 [D], gradients by the weights summed over heads
+ *                    and tokens, or NULL.  The order of the sums is fixed: the
+ *                    same call gives the same bits.
+ *   workspace        device, 16-byte aligned,
+ *                    >= prism_qk_norm_rope_bwd_workspace_bytes(p) bytes
+ *                    (0 for invalid params); may be NULL without dwq and dwk.
+ *                    Not to be shared by calls that may overlap in time.
+ */
+PRISM_API size_t prism_qk_norm_rope_bwd_workspace_bytes(const prism_norm_rope_params* p);
+PRISM_API int prism_qk_norm_rope_bwd(const prism_norm_rope_params* p, const prism_rows* dq_out,
+                                     const prism_rows* dk_out, const prism_rows* q, const prism_rows* k,
+                                     const void* wq, const void* wk, const float* rope, const prism_rows* dq,
+                                     const prism_rows* dk, float* dwq, float* dwk, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
 /* ---- inspection -------------------------------------------------------- */
 #define PRISM_ITEM_SHAPE_ID   0  /* uint8  [heads][Nz]                         */
 #define PRISM_ITEM_NBLOCKS    1  /* int32  [heads]                             */
