@@ -65,6 +65,18 @@ class PrismRows(C.Structure):
     _fields_ = [("data", C.c_void_p), ("head_stride", C.c_int64), ("token_stride", C.c_int64)]
 
 
+PRISM_ACT_NONE = 0
+PRISM_ACT_GELU = 1
+PRISM_ACT_GELU_TANH = 2
+PRISM_ACT_SILU = 3
+
+
+class PrismLinearParams(C.Structure):
+    _fields_ = [("M", C.c_int64), ("K", C.c_int32), ("N", C.c_int32), ("in_heads", C.c_int32), ("out_heads", C.c_int32),
+                ("activation", C.c_int32), ("out_dtype", C.c_int32), ("bias_dtype", C.c_int32), ("dw_dtype", C.c_int32),
+                ("x_stride", C.c_int64), ("w_stride", C.c_int64), ("y_stride", C.c_int64), ("r_stride", C.c_int64)]
+
+
 class PrismError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -118,6 +130,10 @@ def load(path: str | None = None) -> C.CDLL:
         "prism_zone_shapes_noalloc": (i32, [pp, vp, vp, vp, vp, vp]),
         "prism_av_norm": (i32, [C.c_int64, C.c_int32, C.c_int32, C.c_int32, vp, vp, vp, vp, vp,
                                 C.c_int32, vp, vp]),
+        "prism_linear_workspace_bytes": (sz, [C.POINTER(PrismLinearParams)]),
+        "prism_linear": (i32, [C.POINTER(PrismLinearParams), vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]),
+        "prism_linear_bwd_workspace_bytes": (sz, [C.POINTER(PrismLinearParams)]),
+        "prism_linear_bwd": (i32, [C.POINTER(PrismLinearParams), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]),
         "prism_rope_table": (i32, [C.POINTER(PrismNormRopeParams), C.c_float, C.c_int64, vp, vp]),
         "prism_qk_norm_rope": (i32, [C.POINTER(PrismNormRopeParams), C.POINTER(PrismRows), C.POINTER(PrismRows), vp, vp,
                                      vp, C.POINTER(PrismRows), C.POINTER(PrismRows), vp]),
@@ -563,6 +579,13 @@ class _Launch:
         self.tensors.append(t)
         return t
 
+    def zero_status(self):
+        """A device status block for the call, cleared on its stream."""
+        import torch
+        with torch.cuda.stream(self.s):
+            t = torch.zeros(4, dtype=torch.int32, device=self.tensors[0].device)
+        return t
+
     def check(self, status, what):
         if status:
             raise PrismError(status, what)
@@ -712,3 +735,115 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k=None, wq=None, wk=None, rope=None, eps
                                             workspace.numel() * workspace.element_size() if workspace is not None else 0,
                                             go.stream), "prism_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
+
+
+def _features(t, what, dtype=None):
+    """(rows M, features, heads, row stride) of rows [M, F] or a contiguous [heads, M, D]."""
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.dim() == 2:
+        M, F = t.shape
+        if F > 1 and t.stride(1) != 1:
+            raise ValueError(f"{what}: the features of a row must be consecutive")
+        stride = t.stride(0) if M > 1 else F
+        if stride < F:
+            raise ValueError(f"{what}: rows must not overlap")
+        return M, F, 0, stride
+    if t.dim() == 3:
+        if not t.is_contiguous() or t.shape[2] not in (64, 128) or t.shape[0] < 1:
+            raise ValueError(f"{what}: head-major tensors are contiguous [heads, M, 64 or 128]")
+        return t.shape[1], t.shape[0] * t.shape[2], t.shape[0], t.shape[0] * t.shape[2]
+    raise ValueError(f"{what} must be [M, features] or [heads, M, D]")
+
+
+def _shape_like(M, F, heads):
+    return (heads, M, F // heads) if heads else (M, F)
+
+
+def _size(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def linear(x, W, bias=None, residual=None, activation=PRISM_ACT_NONE, y=None, out_dtype=None, out_heads=0, pre=None,
+           want_pre=False, workspace=None, status=None, stream=None):
+    """(y, pre, status): y = act(x W^T + bias) + residual.  x is bf16 rows [M, K] (any row stride) or
+    head-major [heads, M, D]; W bf16 [N, K]; bias [N]; y and residual are rows [M, N], or head-major
+    [out_heads, M, N / out_heads] where out_heads is given (a given y or residual says it too), of
+    out_dtype (bf16 if nothing says otherwise).  A given y may be the residual.  pre is the bf16
+    x W^T + bias for linear_bwd, if wanted.  `status` as in av_norm."""
+    import torch
+    M, K, in_heads, xs = _features(x, "x", torch.bfloat16)
+    N, WK, wh, ws_ = _features(W, "W", torch.bfloat16)
+    if wh or WK != K:
+        raise ValueError(f"W must be [N, {K}], got {tuple(W.shape)}")
+    like = y if y is not None else residual
+    if like is not None:
+        out_dtype = out_dtype or like.dtype
+        if like.dim() == 3:
+            out_heads = out_heads or like.shape[0]
+    out_dtype = out_dtype or torch.bfloat16
+    if out_heads and (out_heads < 0 or N % out_heads or N // out_heads not in (64, 128)):
+        raise ValueError(f"{N} features are not {out_heads} heads of 64 or 128 channels")
+    want = _shape_like(M, N, out_heads)
+    strides = [N, N]
+    for i, (t, what) in enumerate(((y, "y"), (residual, "residual"))):
+        if t is not None:
+            if tuple(t.shape) != want:
+                raise ValueError(f"{what}: expected {want}, got {tuple(t.shape)}")
+            strides[i] = _features(t, what, out_dtype)[3]
+    if pre is not None and (tuple(pre.shape) != want or pre.dtype != torch.bfloat16 or not pre.is_contiguous()):
+        raise ValueError(f"pre must be a contiguous bf16 {want}")
+    if bias is not None and (tuple(bias.shape) != (N,) or not bias.is_contiguous()):
+        raise ValueError(f"bias must be [{N}]")
+    p = PrismLinearParams(M, K, N, in_heads, out_heads, int(activation), _code(out_dtype, "y"),
+                          PRISM_F32 if bias is None else _code(bias.dtype, "bias"), PRISM_F32, xs, ws_, strides[0], strides[1])
+    lib = load()
+    with _Launch([x, W, bias, residual, y, pre, workspace, status], stream) as go:
+        y = go.empty(want, out_dtype) if y is None else y
+        if want_pre and pre is None:
+            pre = go.empty(want, torch.bfloat16)
+        if workspace is None and (xs % 8 or ws_ % 8):
+            workspace = go.empty((max(int(lib.prism_linear_workspace_bytes(C.byref(p))), 16),), torch.uint8)
+        status = go.zero_status() if status is None else status
+        go.check(lib.prism_linear(C.byref(p), _ptr(x), _ptr(W), _ptr(bias), _ptr(residual), _ptr(y), _ptr(pre),
+                                  _ptr(workspace), _size(workspace), _ptr(status), go.stream), "prism_linear")
+    return y, pre, status
+
+
+def linear_bwd(dy, x, W, pre=None, activation=PRISM_ACT_NONE, dx=None, dW=None, db=None, want_dx=True, want_dw=True,
+               want_db=True, dw_dtype=None, workspace=None, status=None, stream=None):
+    """(dx, dW, db, status): the gradients of linear by x (bf16, in x's layout), W ([N, K] of dw_dtype,
+    fp32 if not given) and bias (fp32 [N]), each where wanted, from dy (in y's layout), the forward's x
+    and W, and with an activation its `pre`.  The residual's gradient is dy."""
+    import torch
+    M, K, in_heads, xs = _features(x, "x", torch.bfloat16)
+    N, WK, wh, ws_ = _features(W, "W", torch.bfloat16)
+    Mo, No, out_heads, ys = _features(dy, "dy")
+    if wh or WK != K:
+        raise ValueError(f"W must be [N, {K}], got {tuple(W.shape)}")
+    if (Mo, No) != (M, N):
+        raise ValueError(f"dy has {Mo} rows of {No} features, expected {M} of {N}")
+    want = _shape_like(M, N, out_heads)
+    if activation != PRISM_ACT_NONE:
+        if pre is None or tuple(pre.shape) != want or pre.dtype != torch.bfloat16 or not pre.is_contiguous():
+            raise ValueError(f"the activation's gradient needs pre, a contiguous bf16 {want}")
+    else:
+        pre = None
+    dw_dtype = dw_dtype or (dW.dtype if dW is not None else torch.float32)
+    for t, shape, dtype, what in ((dx, tuple(x.shape), torch.bfloat16, "dx"), (dW, (N, K), dw_dtype, "dW"),
+                                  (db, (N,), torch.float32, "db")):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous {dtype} {shape}")
+    p = PrismLinearParams(M, K, N, in_heads, out_heads, int(activation), _code(dy.dtype, "dy"), PRISM_F32,
+                          _code(dw_dtype, "dW"), xs, ws_, ys, N)
+    lib = load()
+    with _Launch([dy, x, W, pre, dx, dW, db, workspace, status], stream) as go:
+        dx = go.empty(tuple(x.shape), torch.bfloat16) if dx is None and want_dx else dx
+        dW = go.empty((N, K), dw_dtype) if dW is None and want_dw else dW
+        db = go.empty((N,), torch.float32) if db is None and want_db else db
+        if workspace is None:
+            workspace = go.empty((max(int(lib.prism_linear_bwd_workspace_bytes(C.byref(p))), 16),), torch.uint8)
+        status = go.zero_status() if status is None else status
+        go.check(lib.prism_linear_bwd(C.byref(p), _ptr(dy), _ptr(x), _ptr(W), _ptr(pre), _ptr(dx), _ptr(dW), _ptr(db),
+                                      _ptr(workspace), _size(workspace), _ptr(status), go.stream), "prism_linear_bwd")
+    return dx, dW, db, status

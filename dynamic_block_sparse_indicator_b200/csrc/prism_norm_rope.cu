@@ -48,7 +48,7 @@ struct Args {
     int w_f32;
     Rope rope;
     int64_t N;
-    int heads, hpc;                // heads, heads per block
+    int heads, hpc, tensors;       // heads, heads per block, 2 with a key
     float eps;
     float* part;                   // backward: [2][blocks of a tensor][D] partial weight gradients, or null
 };
@@ -95,11 +95,15 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ void load_w(const void* w, int f32, int ch, float* out) {
-    #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        out[i] = !w ? 1.f : f32 ? static_cast<const float*>(w)[ch + i]
-                                : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[ch + i]);
+__device__ __forceinline__ float weight_at(const void* w, int f32, int ch) {
+    return !w ? 1.f : f32 ? static_cast<const float*>(w)[ch] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[ch]);
+}
+// A lane's eight weights from their copy in shared memory (read again for every group of
+// rows: two loads instead of eight registers held over the loop).
+__device__ __forceinline__ void read_w(const float4* sw, int ch, float* w) {
+    const float4 a = sw[ch / 4], b = sw[ch / 4 + 1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
 // A lane's part of the rotation at one token.  Adjacent pairs (2p, 2p + 1) lie in one
@@ -127,8 +131,9 @@ template <> struct Turn<false> {
         for (int i = 0; i < 4; ++i) cs[i] = rope_at(r, (ch >> 1) + i, t, h, w);
     }
     // u -> R u (DIR = 1) or R^T u (DIR = -1)
+    static __device__ __forceinline__ void put(const float*, float*, int) {}
     template <int DIR>
-    __device__ __forceinline__ void apply(float* u, float*, int) const {
+    __device__ __forceinline__ void take(float* u, const float*) const {
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float a = u[2 * i], b = u[2 * i + 1], c = cs[i].x, s = DIR * cs[i].y;
@@ -162,101 +167,139 @@ template <> struct Turn<true> {
             }
         }
     }
-    template <int DIR>
-    __device__ __forceinline__ void apply(float* u, float* row, int ch) const {
-        float* mine = row + place(ch);
-        __syncwarp();                        // the previous row's reads are done
+    static __device__ __forceinline__ void put(const float* u, float* row, int ch) {
         #pragma unroll
-        for (int i = 0; i < 8; ++i) mine[i] = u[i];
-        __syncwarp();
+        for (int i = 0; i < 8; ++i) row[place(ch) + i] = u[i];
+    }
+    template <int DIR>
+    __device__ __forceinline__ void take(float* u, const float* row) const {
         #pragma unroll
         for (int i = 0; i < 8; ++i) u[i] = u[i] * c[i] + DIR * s[i] * row[at[i]];
     }
 };
 
-// Rows of shared memory for the exchange (HALVES only): one row per row of the block.
-template <int D, bool HALVES>
-struct Exchange {
-    static constexpr int kRows = kThreads / (D / 8);
+// Rows of a group, and shared memory for their exchange (HALVES only).
+template <typename T, int D, bool HALVES, int U>
+struct Group {
+    static constexpr int kRows = kThreads / (D / 8);      // rows of one head in a block
     static constexpr int kPitch = D + D / 8;
-    static constexpr int kFloats = HALVES ? kRows * kPitch : 1;
+    static constexpr int kFloats = HALVES ? U * kRows * kPitch : 1;
 };
 
-// Grid: x = token tiles (strided), y = head groups, z = query or key.
+__device__ __forceinline__ void grid_at(const Rope& r, int64_t n, int& t, int& h, int& w) {
+    const uint32_t hw = (uint32_t)r.H * (uint32_t)r.W, m = (uint32_t)n;     // N < 2^31
+    t = (int)(m / hw);
+    const uint32_t q = m - (uint32_t)t * hw;
+    h = (int)(q / (uint32_t)r.W);
+    w = (int)(q - (uint32_t)h * (uint32_t)r.W);
+}
+
+// Grid: x = token tiles (strided), y = head groups.  A block takes its tokens' rows of both
+// tensors, U heads at a time: U loads in flight per lane, one exchange for the group.
 template <typename TI, typename TO, int D, bool HALVES>
-__global__ void __launch_bounds__(kThreads) k_norm_rope(const Args a) {
-    constexpr int LANES = D / 8, RPB = kThreads / LANES, U = 4;
-    __shared__ float sx[Exchange<D, HALVES>::kFloats];
-    const int z = blockIdx.z, ch = (threadIdx.x % LANES) * 8, sub = threadIdx.x / LANES;
-    float* row = HALVES ? sx + sub * Exchange<D, HALVES>::kPitch : nullptr;
-    const Rows in = a.in[z], out = a.out[z];
+__global__ void __launch_bounds__(kThreads, HALVES ? 3 : 4) k_norm_rope(const Args a) {
+    constexpr int U = sizeof(TI) == 2 ? 4 : 2;
+    using G = Group<TI, D, HALVES, U>;
+    constexpr int LANES = D / 8, RPB = G::kRows;
+    __shared__ float sx[G::kFloats];
+    __shared__ float4 sw[2][D / 4];
+    const int ch = (threadIdx.x % LANES) * 8, sub = threadIdx.x / LANES;
+    float* row = HALVES ? sx + sub * G::kPitch : sx;
     const int h0 = blockIdx.y * a.hpc, h1 = min(h0 + a.hpc, a.heads);
-    float w[8];
-    load_w(a.w[z], a.w_f32, ch, w);
+    for (int i = threadIdx.x; i < a.tensors * D; i += kThreads)
+        reinterpret_cast<float*>(sw)[i] = weight_at(a.w[i / D], a.w_f32, i % D);
+    __syncthreads();
     for (int64_t n0 = (int64_t)blockIdx.x * RPB; n0 < a.N; n0 += (int64_t)gridDim.x * RPB) {
         const int64_t n = n0 + sub;
         const bool ok = n < a.N;
         Turn<HALVES> turn;
         if (a.rope.tab) {
-            const int64_t m = ok ? n : 0, hw = (int64_t)a.rope.H * a.rope.W;
-            const int t = (int)(m / hw), r = (int)(m - t * hw);
-            turn.init(a.rope, ch, t, r / a.rope.W, r % a.rope.W);
+            int t, h, w;
+            grid_at(a.rope, ok ? n : 0, t, h, w);
+            turn.init(a.rope, ch, t, h, w);
         }
-        const TI* src = static_cast<const TI*>(in.p) + n * in.ts + ch;
-        TO* dst = static_cast<TO*>(out.p) + n * out.ts + ch;
-        for (int h = h0; h < h1; h += U) {
-            Vec8<TI> v[U];
-            #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                v[i] = Vec8<TI>{};
-                if (ok && h + i < h1) v[i].load(src + (h + i) * in.hs);
-            }
-            #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                if (h + i >= h1) break;      // the same for the whole block
-                float x[8], ss = 0.f;
-                v[i].get(x);
+        for (int z = 0; z < a.tensors; ++z) {
+            const TI* src = static_cast<const TI*>(a.in[z].p) + n * a.in[z].ts + ch;
+            TO* dst = static_cast<TO*>(a.out[z].p) + n * a.out[z].ts + ch;
+            for (int h = h0; h < h1; h += U) {
+                Vec8<TI> v[U];
+                float r[U];
                 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                const float r = rsqrtf(row_sum<LANES>(ss) * (1.f / D) + a.eps);
+                for (int i = 0; i < U; ++i) {
+                    v[i] = Vec8<TI>{};
+                    if (ok && h + i < h1) v[i].load(src + (h + i) * a.in[z].hs);
+                }
                 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
-                if (a.rope.tab) turn.template apply<1>(x, row, ch);
-                if (ok) Vec8<TO>::store(dst + (h + i) * out.hs, x);
+                for (int i = 0; i < U; ++i) {
+                    float x[8];
+                    v[i].get(x);
+                    r[i] = x[0] * x[0];
+                    #pragma unroll
+                    for (int e = 1; e < 8; ++e) r[i] = fmaf(x[e], x[e], r[i]);
+                }
+                #pragma unroll
+                for (int i = 0; i < U; ++i) r[i] = rsqrtf(row_sum<LANES>(r[i]) * (1.f / D) + a.eps);
+                float w[8];
+                read_w(sw[z], ch, w);
+                if (HALVES && a.rope.tab) {
+                    __syncwarp();                    // the previous group's reads are done
+                    #pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        float x[8];
+                        v[i].get(x);
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = x[e] * r[i] * w[e];
+                        turn.put(x, row + i * RPB * G::kPitch, ch);
+                    }
+                    __syncwarp();
+                }
+                #pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    if (h + i >= h1) break;          // the same for the whole block
+                    float x[8];
+                    v[i].get(x);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = x[e] * r[i] * w[e];
+                    if (a.rope.tab) turn.template take<1>(x, row + i * RPB * G::kPitch);
+                    if (ok) Vec8<TO>::store(dst + (h + i) * a.out[z].hs, x);
+                }
             }
         }
     }
 }
 
-// The gradients.  TI: type of x and dx; TG: type of dy.  A block sums its rows' part of
-// dw in registers (in the order of its loop), then over its rows through shared memory,
-// and writes one row of partial sums: no atomics, the same bits every time.
+// The gradients.  TI: type of x and dx; TG: type of dy.  Grid: z = query or key (a block
+// then holds one weight's sums).  A block sums its rows' part of dw in registers (in the
+// order of its loop), then over its rows through shared memory, and writes one row of
+// partial sums: no atomics, the same bits every time.
 template <typename TI, typename TG, int D, bool HALVES>
-__global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const Args a) {
-    constexpr int LANES = D / 8, RPB = kThreads / LANES, U = 2;
+__global__ void __launch_bounds__(kThreads, 2) k_norm_rope_bwd(const Args a) {
+    constexpr int U = 4;
+    using G = Group<TG, D, HALVES, U>;
+    constexpr int LANES = D / 8, RPB = G::kRows;
     constexpr int kSum = RPB * D;
-    constexpr int kEx = Exchange<D, HALVES>::kFloats;
-    __shared__ float sx[kSum > kEx ? kSum : kEx];
+    __shared__ float sx[kSum > G::kFloats ? kSum : G::kFloats];
+    __shared__ float4 sw[1][D / 4];
     const int z = blockIdx.z, ch = (threadIdx.x % LANES) * 8, sub = threadIdx.x / LANES;
-    float* row = HALVES ? sx + sub * Exchange<D, HALVES>::kPitch : nullptr;
-    const Rows in = a.in[z], out = a.out[z], grad = a.grad[z];
+    float* row = HALVES ? sx + sub * G::kPitch : sx;
     const int h0 = blockIdx.y * a.hpc, h1 = min(h0 + a.hpc, a.heads);
-    float w[8], dw[8];
-    load_w(a.w[z], a.w_f32, ch, w);
+    float dw[8];
     #pragma unroll
     for (int e = 0; e < 8; ++e) dw[e] = 0.f;
+    if (threadIdx.x < D) reinterpret_cast<float*>(sw)[threadIdx.x] = weight_at(a.w[z], a.w_f32, threadIdx.x);
+    __syncthreads();
     for (int64_t n0 = (int64_t)blockIdx.x * RPB; n0 < a.N; n0 += (int64_t)gridDim.x * RPB) {
         const int64_t n = n0 + sub;
         const bool ok = n < a.N;
         Turn<HALVES> turn;
         if (a.rope.tab) {
-            const int64_t m = ok ? n : 0, hw = (int64_t)a.rope.H * a.rope.W;
-            const int t = (int)(m / hw), r = (int)(m - t * hw);
-            turn.init(a.rope, ch, t, r / a.rope.W, r % a.rope.W);
+            int t, h, w;
+            grid_at(a.rope, ok ? n : 0, t, h, w);
+            turn.init(a.rope, ch, t, h, w);
         }
-        const TI* src = static_cast<const TI*>(in.p) + n * in.ts + ch;
-        const TG* gsr = static_cast<const TG*>(grad.p) + n * grad.ts + ch;
-        TI* dst = static_cast<TI*>(out.p) + n * out.ts + ch;
+        const TI* src = static_cast<const TI*>(a.in[z].p) + n * a.in[z].ts + ch;
+        const TG* gsr = static_cast<const TG*>(a.grad[z].p) + n * a.grad[z].ts + ch;
+        TI* dst = static_cast<TI*>(a.out[z].p) + n * a.out[z].ts + ch;
         for (int h = h0; h < h1; h += U) {
             Vec8<TI> v[U];
             Vec8<TG> q[U];
@@ -265,17 +308,29 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const Args a) {
                 v[i] = Vec8<TI>{};
                 q[i] = Vec8<TG>{};
                 if (ok && h + i < h1) {
-                    v[i].load(src + (h + i) * in.hs);
-                    q[i].load(gsr + (h + i) * grad.hs);
+                    v[i].load(src + (h + i) * a.in[z].hs);
+                    q[i].load(gsr + (h + i) * a.grad[z].hs);
                 }
             }
+            if (HALVES && a.rope.tab) {
+                __syncwarp();                        // the previous group's reads are done
+                #pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    float g[8];
+                    q[i].get(g);
+                    turn.put(g, row + i * RPB * G::kPitch, ch);
+                }
+                __syncwarp();
+            }
+            float w[8];
+            read_w(sw[0], ch, w);
             #pragma unroll
             for (int i = 0; i < U; ++i) {
-                if (h + i >= h1) break;      // the same for the whole block
+                if (h + i >= h1) break;              // the same for the whole block
                 float x[8], g[8], ss = 0.f, dot = 0.f;
                 v[i].get(x);
                 q[i].get(g);
-                if (a.rope.tab) turn.template apply<-1>(g, row, ch);
+                if (a.rope.tab) turn.template take<-1>(g, row + i * RPB * G::kPitch);
                 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     ss = fmaf(x[e], x[e], ss);
@@ -291,12 +346,12 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const Args a) {
                     dw[e] = fmaf(g[e], x[e] * r, dw[e]);
                     x[e] = r * (g[e] * w[e] - k * x[e]);
                 }
-                if (ok) Vec8<TI>::store(dst + (h + i) * out.hs, x);
+                if (ok) Vec8<TI>::store(dst + (h + i) * a.out[z].hs, x);
             }
         }
     }
     if (a.part) {
-        __syncthreads();                     // the exchange rows are free
+        __syncthreads();                             // the exchange rows are free
         #pragma unroll
         for (int e = 0; e < 8; ++e) sx[sub * D + ch + e] = dw[e];
         __syncthreads();
@@ -541,11 +596,12 @@ extern "C" int prism_qk_norm_rope(const prism_norm_rope_params* p, const prism_r
     a.w[0] = wq;
     a.w[1] = wk;
     a.w_f32 = p->w_dtype == PRISM_F32;
+    a.tensors = z;
     a.rope = rope_of(p, rope);
     a.N = p->N;
     a.heads = p->heads;
     a.eps = p->eps;
-    const Grid g = grid_of(p->N, p->heads, D, z);
+    const Grid g = grid_of(p->N, p->heads, D, 1);
     a.hpc = g.hpc;
     nvtxRangePushA("prism qk norm rope");
     const int st = dispatch<false>(p, a, g, static_cast<cudaStream_t>(stream));
@@ -611,6 +667,7 @@ extern "C" int prism_qk_norm_rope_bwd(const prism_norm_rope_params* p, const pri
     a.w[0] = wq;
     a.w[1] = wk;
     a.w_f32 = p->w_dtype == PRISM_F32;
+    a.tensors = z;
     a.rope = rope_of(p, rope);
     a.N = p->N;
     a.heads = p->heads;

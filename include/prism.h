@@ -484,6 +484,79 @@ PRISM_API int prism_qk_norm_rope_bwd(const prism_norm_rope_params* p, const pris
                                      const prism_rows* dk, float* dwq, float* dwk, void* workspace,
                                      size_t ws_bytes, void* stream);
 
+/* ---- projections ---------------------------------------------------------- */
+/*
+ * prism_linear -- the projections around the attention:
+ *     z = x W^T + bias,   y = act(z) + residual,
+ *   bf16 products with fp32 sums; bias, activation and residual in fp32, one
+ *   rounding to out_dtype.  x and y are each rows ([M][K], [M][N]) or head-major
+ *   ([heads][M][64 or 128]: feature f is channel f % D of head f / D), so the
+ *   input projection writes what prism_plan reads ([3 heads][N][D] holds Q, K and
+ *   V one after the other) and the output projection reads what prism_attn_fwd
+ *   writes, without a transposing copy.
+ * prism_linear_params
+ *   M          rows (tokens), 0 .. 2^31 - 256 (0: the call does nothing).
+ *   K, N       input and output features, 1 .. 2^24.
+ *   in_heads   0: x is rows, x_stride >= K elements apart; else x is contiguous
+ *              [in_heads][M][K / in_heads], K / in_heads 64 or 128.
+ *   out_heads  the same for y, residual and pre with N.
+ *   activation PRISM_ACT_NONE, PRISM_ACT_GELU (z Phi(z)), PRISM_ACT_GELU_TANH
+ *              (its tanh form) or PRISM_ACT_SILU (z / (1 + e^-z)).
+ *   out_dtype  element type of y, residual and dy;  bias_dtype of bias;
+ *   dw_dtype   of dW: PRISM_BF16 or PRISM_F32 each.
+ *   x_stride, w_stride, y_stride, r_stride   elements between the rows of x, W
+ *              ([N][K]), y or dy, residual; the contiguous count (K, K, N, N)
+ *              where the tensor is head-major.
+ * Arguments (device, 16-byte aligned)
+ *   x, W       bf16.
+ *   bias       [N] or NULL.  residual, in y's layout, or NULL; may be y itself.
+ *   y          written; rows beyond M and columns beyond N are not.
+ *   pre        bf16, contiguous in y's layout: receives z for the backward, or
+ *              NULL.
+ *   workspace  >= prism_linear_workspace_bytes(p) bytes; may be NULL where
+ *              x_stride and w_stride are multiples of 8 (or x is head-major).
+ *              Not to be shared by calls that may overlap in time.
+ *   dev_status device int32[4], zero before the call (see prism_av_norm).
+ * Sums run in a fixed order: the same call gives the same bits.  What is written
+ * may not overlap what else the call reads or writes, y over residual excepted.
+ */
+#define PRISM_ACT_NONE      0
+#define PRISM_ACT_GELU      1
+#define PRISM_ACT_GELU_TANH 2
+#define PRISM_ACT_SILU      3
+typedef struct prism_linear_params {
+    int64_t M;
+    int32_t K, N;
+    int32_t in_heads, out_heads;
+    int32_t activation;
+    int32_t out_dtype;
+    int32_t bias_dtype;
+    int32_t dw_dtype;
+    int64_t x_stride, w_stride, y_stride, r_stride;
+} prism_linear_params;
+
+PRISM_API size_t prism_linear_workspace_bytes(const prism_linear_params* p);
+PRISM_API int prism_linear(const prism_linear_params* p, const void* x, const void* W, const void* bias,
+                           const void* residual, void* y, void* pre, void* workspace, size_t ws_bytes,
+                           int32_t* dev_status, void* stream);
+
+/*
+ * prism_linear_bwd -- its gradients (the residual's is dy itself):
+ *     dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum over rows of dz.
+ *   dy   out_dtype, in y's layout.  pre: the forward's z (unread without an
+ *        activation).  dz enters the products in bf16: exactly dy without an
+ *        activation and with a bf16 dy, rounded to nearest otherwise; db sums
+ *        the unrounded values.
+ *   dx   bf16, contiguous in x's layout; dW [N][K] of dw_dtype, contiguous; db
+ *        fp32 [N]: written, each NULL if not wanted (M = 0 writes zeros to dW
+ *        and db).  W may be NULL without dx, x without dW.
+ *   workspace  >= prism_linear_bwd_workspace_bytes(p) bytes, always given.
+ */
+PRISM_API size_t prism_linear_bwd_workspace_bytes(const prism_linear_params* p);
+PRISM_API int prism_linear_bwd(const prism_linear_params* p, const void* dy, const void* x, const void* W,
+                               const void* pre, void* dx, void* dW, float* db, void* workspace, size_t ws_bytes,
+                               int32_t* dev_status, void* stream);
+
 /* ---- inspection -------------------------------------------------------- */
 #define PRISM_ITEM_SHAPE_ID   0  /* uint8  [heads][Nz]                         */
 #define PRISM_ITEM_NBLOCKS    1  /* int32  [heads]                             */
