@@ -5,17 +5,19 @@
 // input projection writes what prism_plan reads and the output projection reads what
 // prism_attn_fwd writes, without a transposing copy.
 //
-// All products are one kernel: C[r][c] = sum_k B[r][k] A[c][k], c the contiguous index of
-// C.  The tensor core's M dimension (TMEM lanes) runs over c and its N dimension (TMEM
-// columns) over r, so an epilogue warp holds 32 consecutive c of one row in its lanes:
-// bias is one value per lane, residual and results are consecutive addresses, and few
-// tokens are a small N instead of an M tile of padding.  An operand is a 3-D TMA map
-// (inner, rows, heads) with the contraction along the inner index (K-major) or along the
-// rows (MN-major); head-major inner coordinates split into (channel, head):
-//     forward  A = W  [N][K] K-major     B = x  [M][K] K-major
-//     dx       A = W  [N][K] MN-major    B = dz [M][N] K-major
-//     dW       A = x  [M][K] MN-major    B = dz [M][N] MN-major
-// Bound: the tensor cores for many tokens (2 M K N flops), HBM's read of W for few.
+// Every product is C[r][c] = sum_k X[r][k] Y[c][k], c the contiguous index of C.  An operand
+// is a 3-D TMA map (inner, rows, heads) with the contraction along the inner index (K-major)
+// or along the rows (MN-major); head-major inner coordinates split into (channel, head):
+//     forward  X = x  [M][K] K-major     Y = W [N][K] K-major
+//     dx       X = dz [M][N] K-major     Y = W [N][K] MN-major
+//     dW       X = dz [M][N] MN-major    Y = x [M][K] MN-major
+// Two kernels:
+//   k_tile  many rows: TMEM lanes are rows, columns are c.  A pair of CTAs (cta_group::2)
+//           shares a 256 x BN tile, or one CTA has 128 x 128, whose contraction a cluster may
+//           split.  A warp's results leave through a 4 KB stage and TMA stores.
+//   k_few   up to 64 rows: TMEM lanes are c and columns are rows, so few tokens are a small
+//           N of the instruction instead of an M tile of padding.  Bound by HBM's read of W;
+//           a cluster splits the contraction.
 //
 // Warp roles: 0-7 epilogue (TMEM lane quarter w % 4, column half w / 4), 8 TMA producer and
 // TMEM allocator, 9 MMA issuer.  Two TMEM accumulators alternate, so the next products run
@@ -23,9 +25,10 @@
 //
 // The tensor core's fp32 accumulation truncates: over a contraction of 16,384 the result
 // is low by 1.6e-5 of its size, growing linearly (measured with standard normal operands;
-// 4.7e-6 at 5,120).  So a contraction is cut into chunks of at most kChunk elements, each
-// summed by the tensor core into a fresh accumulator, and the chunks are added in
-// registers with round-to-nearest.
+// 4.7e-6 at 5,120).  So a contraction is cut into chunks, each summed by the tensor core into
+// a fresh accumulator, and the chunks are added in registers with round-to-nearest: chunks of
+// 2,048 elements where the result is fp32 (2e-6 low), of 16,384 where it is rounded to bf16
+// (1.6e-5, a hundredth of half a step).
 //
 // Every barrier wait is bounded (PRISM_ERR_TIMEOUT with a site in the status block).
 #include <cuda.h>
@@ -42,7 +45,8 @@ namespace lin {
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarps + 2) * 32;
 constexpr int kKB = 64;                    // contraction elements per stage (128-byte rows)
-constexpr int kChunkKB = 32;               // stages per accumulation chunk: 2,048 elements
+constexpr int kChunkF32 = 32;              // stages per accumulation chunk (see above): 2,048 elements
+constexpr int kChunkBF16 = 256;            // and 16,384 where the result keeps 16 bits
 
 struct Operand {
     int inner;                             // extent of the inner index of one head
@@ -54,16 +58,19 @@ struct Out {
     int64_t rs, hs;
     int hd;                                // channels per head; 0 = one head
     int f32;
+    int vec;                               // 16-byte accesses at multiples of 16 bytes of a row
 };
 
 struct Args {
-    Operand a, b;
+    Operand a, b;                          // the operand along the tensor core's M, and along its N
     int64_t R;                             // rows of C
     int C;                                 // columns of C
     int kblocks;                           // stages of the whole contraction
     int split;                             // CTAs of a cluster that share a tile's contraction
+    int chunk;                             // stages per accumulation chunk
     int tiles_c, tiles_r, band;
     Out y, pre, res;
+    int y_tma;                             // the results' rows can leave by TMA
     const void* bias;
     int bias_f32, act;
     int* err;
@@ -191,27 +198,29 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
 }
 
 // ---------------------------------------------------------------- activations
+// tanh(u) = 2 / (1 + e^-2u) - 1, so the tanh form is z / (1 + e^-2u), like SiLU's z / (1 + e^-z):
+// one __expf (its error grows with |argument|, where the quotient no longer depends on it) and
+// one quotient.
+__device__ __forceinline__ float logistic(float t) { return __fdividef(1.f, 1.f + __expf(-t)); }
+__device__ __forceinline__ float tanh_arg(float z) { return 1.5957691216057308f * (z + 0.044715f * z * z * z); }
 __device__ __forceinline__ float act_of(float z, int act) {
     switch (act) {
         case PRISM_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-        case PRISM_ACT_GELU_TANH: {
-            const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
-            return 0.5f * z * (1.f + tanhf(u));
-        }
-        case PRISM_ACT_SILU: return z / (1.f + expf(-z));
+        case PRISM_ACT_GELU_TANH: return z * logistic(tanh_arg(z));
+        case PRISM_ACT_SILU: return z * logistic(z);
         default: return z;
     }
 }
 __device__ __forceinline__ float act_grad(float z, int act) {
     switch (act) {
         case PRISM_ACT_GELU:
-            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
+            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
         case PRISM_ACT_GELU_TANH: {
-            const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
-            return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * 0.79788456080286536f * (1.f + 0.134145f * z * z);
+            const float s = logistic(tanh_arg(z));
+            return s + z * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z * z);
         }
         case PRISM_ACT_SILU: {
-            const float s = 1.f / (1.f + expf(-z));
+            const float s = logistic(z);
             return s * (1.f + z * (1.f - s));
         }
         default: return 1.f;
@@ -249,7 +258,7 @@ __device__ __forceinline__ Lane lane_of(const Args& a, int c) {
 // residual, one rounding.  The rows' residuals are read before any of them is used (the
 // result may be the residual's own memory: each element is read before it is written).
 template <int NC>
-__device__ __forceinline__ void emit(const Args& a, const Lane& l, int64_t r0, int n, const uint32_t* v) {
+__device__ __forceinline__ void emit(const Args& a, const Lane& l, int64_t r0, int n, const float* v) {
     if (!l.on) return;
     float res[NC];
     if (l.res) {
@@ -267,7 +276,7 @@ __device__ __forceinline__ void emit(const Args& a, const Lane& l, int64_t r0, i
     for (int j = 0; j < NC; ++j) {
         if (j < n) {
             const int64_t r = r0 + j;
-            float z = __uint_as_float(v[j]) + l.bias;
+            float z = v[j] + l.bias;
             // the kept z has the operands' 16 bits: the backward forms dz from it for 16-bit products
             if (l.pre) *reinterpret_cast<__nv_bfloat16*>(l.pre + r * l.ps) = __float2bfloat16_rn(z);
             if (a.act != PRISM_ACT_NONE) z = act_of(z, a.act);
@@ -279,242 +288,537 @@ __device__ __forceinline__ void emit(const Args& a, const Lane& l, int64_t r0, i
     }
 }
 
-template <int CG, int BR>
+// The roles that both kernels share.  BM x BN: the tile along the tensor core's M (of all CTAs
+// of the group) and N.
+template <int CG, int BN>
 struct Cfg {
+    static constexpr int kM = 128 * CG;
     static constexpr int kA = 128 * kKB * 2;                 // bytes of a stage: A, then B
-    static constexpr int kB = (BR / CG) * kKB * 2;
+    static constexpr int kB = (BN / CG) * kKB * 2;
     static constexpr int kStage = kA + kB;
-    // CG 2: one CTA per SM; CG 1: two per SM (TMEM 2 x 2 BR <= 512 columns)
+    // CG 2: one CTA per SM; CG 1: two per SM (TMEM 2 x 2 BN <= 512 columns)
     static constexpr int kStages = (CG == 2 ? 196608 : 98304) / kStage;
-    static constexpr int kCols = 2 * BR;
-    static constexpr int kHalf = BR / 2;                     // columns per epilogue warp
-    static constexpr int kSmem = kStages * kStage + 1024;
+    static constexpr int kCols = 2 * BN;
+    static constexpr int kHalf = BN / 2;                     // columns per epilogue warp
+    static constexpr int kRing = kStages * kStage;
 };
 
-// Grid: clusters of CG (a pair on one tile) or split CTAs (one tile, each a part of the
-// contraction); clusters walk the tiles.
-template <int CG, int BR>
-__global__ void __launch_bounds__(kThreads, CG == 2 ? 1 : 2)
-k_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a) {
-    using F = Cfg<CG, BR>;
-    constexpr int ST = F::kStages;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2];
-    __shared__ uint32_t tmem_base;
-    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool clustered = CG == 2 || a.split > 1;
-    const uint32_t rank = clustered ? cluster_rank() : 0;
-    const int group = CG == 2 ? 2 : a.split;
-    const int first = blockIdx.x / group, step = gridDim.x / group;
-    const int ntiles = a.tiles_c * a.tiles_r;
-    // this CTA's part of the contraction
-    const int kb0 = CG == 2 ? 0 : (int)((int64_t)a.kblocks * rank / a.split);
-    const int kb1 = CG == 2 ? a.kblocks : (int)((int64_t)a.kblocks * (rank + 1) / a.split);
-    const int nk = kb1 - kb0, nch = (nk + kChunkKB - 1) / kChunkKB;
-    constexpr int W_PROD = kEpiWarps, W_MMA = kEpiWarps + 1;
+template <int ST>
+struct Bars {
+    uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2];
+    uint32_t tmem_base;
+};
 
+// What a CTA works on.
+struct Work {
+    uint32_t rank;                         // in its cluster
+    int first, step, ntiles;               // tiles first, first + step, ...
+    int kb0, kb1, nk, nch;                 // stages of the contraction, accumulation chunks
+};
+template <int CG>
+__device__ __forceinline__ Work work_of(const Args& a) {
+    Work w;
+    w.rank = CG == 2 || a.split > 1 ? cluster_rank() : 0;
+    const int group = CG == 2 ? 2 : a.split;
+    w.first = blockIdx.x / group;
+    w.step = gridDim.x / group;
+    w.ntiles = a.tiles_c * a.tiles_r;
+    w.kb0 = CG == 2 ? 0 : (int)((int64_t)a.kblocks * w.rank / a.split);
+    w.kb1 = CG == 2 ? a.kblocks : (int)((int64_t)a.kblocks * (w.rank + 1) / a.split);
+    w.nk = w.kb1 - w.kb0;
+    w.nch = (w.nk + a.chunk - 1) / a.chunk;
+    return w;
+}
+// Tile t: bands of `band` row tiles, the columns of a band one after the other, so the tiles
+// that run at one time share their operands' rows in L2.
+__device__ __forceinline__ void tile_at(const Args& a, int t, int& tc, int& tr) {
+    const int per = a.band * a.tiles_c, b = t / per, q = t - b * per;
+    const int rows = min(a.band, a.tiles_r - b * a.band);
+    tc = q / rows;
+    tr = b * a.band + q - tc * rows;
+}
+
+// Barriers and TMEM; returns the TMEM address.
+template <int CG, int BN, int ST>
+__device__ __forceinline__ uint32_t start(Bars<ST>& sm, int warp) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], kEpiWarps * CG);
+            mbar_init(&sm.acc_full[i], 1);
+            mbar_init(&sm.acc_empty[i], kEpiWarps * CG);
         }
         mbar_fence_init();
     }
-    if (warp == W_PROD) {
+    if (warp == kEpiWarps) {
         __syncwarp();
-        alloc_tmem<CG>(&tmem_base, F::kCols);
+        alloc_tmem<CG>(&sm.tmem_base, 2 * BN);
     }
     tc_fence_before();
     __syncwarp();
     if (CG == 2) cluster_sync();
     else __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base;
+    return sm.tmem_base;
+}
+template <int CG, int BN>
+__device__ __forceinline__ void finish_cta(uint32_t tmem, int warp) {
+    tc_fence_before();
+    __syncwarp();
+    if (CG == 2) cluster_sync();           // the pair's other CTA may still signal this one's barriers
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == kEpiWarps) {
+        __syncwarp();
+        free_tmem<CG>(tmem, 2 * BN);
+    }
+}
 
-    // tile t: bands of `band` row tiles, the columns of a band one after the other, so the
-    // tiles that run at one time share their operands' rows in L2
-    auto tile_at = [&](int t, int& tc, int& tr) {
-        const int per = a.band * a.tiles_c, b = t / per, q = t - b * per;
-        const int rows = min(a.band, a.tiles_r - b * a.band);
-        tc = q / rows;
-        tr = b * a.band + q - tc * rows;
-    };
-
-    if (warp == W_PROD) {
-        if (lane == 0) {
-            tma_prefetch_desc(&tm_a);
-            tma_prefetch_desc(&tm_b);
-            int it = 0;
-            bool ok = true;
-            for (int t = first; ok && t < ntiles; t += step) {
-                int tc, tr;
-                tile_at(t, tc, tr);
-                const int c0 = tc * 128 * CG + (CG == 2 ? 128 * (int)rank : 0);
-                const int64_t r0 = (int64_t)tr * BR + (CG == 2 ? (BR / 2) * (int)rank : 0);
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % ST;
-                    if (it >= ST && !mbar_wait(&empty[s], (it / ST - 1) & 1, a.err, 3101)) { ok = false; break; }
-                    uint32_t bar = smem_u32(&full[s]);
-                    if (CG == 2) bar = map_to(bar, 0);
-                    // the pair's first CTA expects the bytes of both
-                    if (CG == 1 || rank == 0) mbar_expect_tx(&full[s], CG * F::kStage);
-                    const uint32_t da = ring + s * F::kStage, db = da + F::kA;
-                    const int k = kb * kKB;
-                    if (a.a.mn) {
-                        #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int c = c0 + 64 * i;
-                            tma3<CG>(da + i * 8192, &tm_a, bar, c % a.a.inner, k, c / a.a.inner);
-                        }
-                    } else {
-                        tma3<CG>(da, &tm_a, bar, k % a.a.inner, c0, k / a.a.inner);
-                    }
-                    if (a.b.mn) {
-                        #pragma unroll
-                        for (int i = 0; i < (BR / CG + 63) / 64; ++i) {
-                            const int r = (int)r0 + 64 * i;
-                            tma3<CG>(db + i * 8192, &tm_b, bar, r % a.b.inner, k, r / a.b.inner);
-                        }
-                    } else {
-                        tma3<CG>(db, &tm_b, bar, k % a.b.inner, (int)r0, k / a.b.inner);
-                    }
-                }
-            }
-            // every copy has landed before the block may end (an MMA issuer that gave up waits for none)
-            if (CG == 1 || rank == 0)
-                for (int i = it > ST ? it - ST : 0; i < it; ++i)
-                    if (!mbar_try(&full[i % ST], (i / ST) & 1) && !mbar_wait(&full[i % ST], (i / ST) & 1, a.err, 3102)) break;
-        }
-    } else if (warp == W_MMA) {
-        if (lane == 0 && (CG == 1 || rank == 0)) {
-            const uint32_t idesc = idesc_bf16(128 * CG, BR, a.a.mn, a.b.mn);
-            const uint32_t sa = a.a.mn ? 128 : 2, sb = a.b.mn ? 128 : 2;        // 16-byte units per 16 of k
-            const uint32_t la = a.a.mn ? 8192 : 16, lb = a.b.mn ? 8192 : 16;
-            int it = 0, ac = 0;
-            bool ok = true;
-            for (int t = first; ok && t < ntiles; t += step) {
-                for (int ch = 0; ok && ch < nch; ++ch, ++ac) {
-                    const int n = (int)((int64_t)nk * (ch + 1) / nch - (int64_t)nk * ch / nch), buf = ac & 1;
-                    if (ac >= 2 && !mbar_wait(&acc_empty[buf], (ac / 2 - 1) & 1, a.err, 3201)) { ok = false; break; }
-                    tc_fence_after();
-                    for (int i = 0; i < n; ++i, ++it) {
-                        const int s = it % ST;
-                        if (!mbar_wait(&full[s], (it / ST) & 1, a.err, 3202)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint32_t da = desc_lo(ring + s * F::kStage, la);
-                        const uint32_t db = desc_lo(ring + s * F::kStage + F::kA, lb);
-                        #pragma unroll
-                        for (int kk = 0; kk < kKB / 16; ++kk)
-                            mma<CG>(tmem + buf * BR, desc_from_lo(da + kk * sa), desc_from_lo(db + kk * sb), idesc,
-                                    i > 0 || kk > 0 ? 1u : 0u);
-                        commit<CG>(&empty[s]);
-                    }
-                    if (ok) commit<CG>(&acc_full[buf]);
-                }
-            }
+// One operand's part of a stage: ROWS rows of the tile from `o0` on.
+template <int CG, int ROWS>
+__device__ __forceinline__ void load_operand(uint32_t dst, const void* tm, uint32_t bar, const Operand& o, int o0, int k) {
+    if (o.mn) {
+        #pragma unroll
+        for (int i = 0; i < (ROWS + 63) / 64; ++i) {
+            const int c = o0 + 64 * i, z = o.inner ? c / o.inner : 0;
+            tma3<CG>(dst + i * 8192, tm, bar, c - z * o.inner, k, z);
         }
     } else {
-        // ------------------------------------------------ epilogue
-        // One chunk: straight from the accumulator, E columns at a time in a rolled loop (the
-        // activations' code stays small).  Several: all but the last are added up in registers,
-        // the sum goes back to the accumulator's columns and takes the same loop.
-        constexpr int H = F::kHalf, CH = H < 16 ? H : 16, E = H < 16 ? H : 16;
+        const int z = o.inner ? k / o.inner : 0;
+        tma3<CG>(dst, tm, bar, k - z * o.inner, o0, z);
+    }
+}
+
+// The TMA producer (one thread).  ROWS_ARE_M: C's rows lie along the tensor core's M.
+template <int CG, int BN, bool ROWS_ARE_M, int ST>
+__device__ __forceinline__ void produce(const void* tm_a, const void* tm_b, const Args& a, const Work& w, Bars<ST>& sm,
+                                        uint32_t ring) {
+    using F = Cfg<CG, BN>;
+    tma_prefetch_desc(tm_a);
+    tma_prefetch_desc(tm_b);
+    int s = 0, round = 0;
+    bool ok = true;
+    for (int t = w.first; ok && t < w.ntiles; t += w.step) {
+        int tc, tr;
+        tile_at(a, t, tc, tr);
+        const int m0 = (ROWS_ARE_M ? tr : tc) * F::kM + (CG == 2 ? 128 * (int)w.rank : 0);
+        const int n0 = (ROWS_ARE_M ? tc : tr) * BN + (CG == 2 ? (BN / 2) * (int)w.rank : 0);
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+            if (round && !mbar_wait(&sm.empty[s], (round - 1) & 1, a.err, 3101)) { ok = false; break; }
+            uint32_t bar = smem_u32(&sm.full[s]);
+            if (CG == 2) bar = map_to(bar, 0);
+            // the pair's first CTA expects the bytes of both
+            if (CG == 1 || w.rank == 0) mbar_expect_tx(&sm.full[s], CG * F::kStage);
+            const uint32_t da = ring + s * F::kStage;
+            load_operand<CG, 128>(da, tm_a, bar, a.a, m0, kb * kKB);
+            load_operand<CG, BN / CG>(da + F::kA, tm_b, bar, a.b, n0, kb * kKB);
+            if (++s == ST) { s = 0; ++round; }
+        }
+    }
+    // every copy has landed before the block may end (an MMA issuer that gave up waits for none)
+    if (CG == 1 || w.rank == 0)
+        for (int i = 0; i < ST; ++i) {
+            const int uses = round + (i < s ? 1 : 0);
+            if (uses && !mbar_wait(&sm.full[i], (uses - 1) & 1, a.err, 3102)) break;
+        }
+}
+
+// The MMA issuer (one thread; of a pair, the first CTA's).
+template <int CG, int BN, int ST>
+__device__ __forceinline__ void issue(const Args& a, const Work& w, Bars<ST>& sm, uint32_t ring, uint32_t tmem) {
+    using F = Cfg<CG, BN>;
+    const uint32_t idesc = idesc_bf16(128 * CG, BN, a.a.mn, a.b.mn);
+    const uint32_t sa = a.a.mn ? 128 : 2, sb = a.b.mn ? 128 : 2;        // 16-byte units per 16 of k
+    const uint32_t la = a.a.mn ? 8192 : 16, lb = a.b.mn ? 8192 : 16;
+    int s = 0, par = 0, ac = 0;
+    bool ok = true;
+    for (int t = w.first; ok && t < w.ntiles; t += w.step) {
+        for (int ch = 0; ok && ch < w.nch; ++ch, ++ac) {
+            const int n = (int)((int64_t)w.nk * (ch + 1) / w.nch - (int64_t)w.nk * ch / w.nch), buf = ac & 1;
+            if (ac >= 2 && !mbar_wait(&sm.acc_empty[buf], (ac / 2 - 1) & 1, a.err, 3201)) { ok = false; break; }
+            tc_fence_after();
+            for (int i = 0; i < n; ++i) {
+                if (!mbar_wait(&sm.full[s], par, a.err, 3202)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t da = desc_lo(ring + s * F::kStage, la);
+                const uint32_t db = desc_lo(ring + s * F::kStage + F::kA, lb);
+                #pragma unroll
+                for (int kk = 0; kk < kKB / 16; ++kk)
+                    mma<CG>(tmem + buf * BN, desc_from_lo(da + kk * sa), desc_from_lo(db + kk * sb), idesc,
+                            i > 0 || kk > 0 ? 1u : 0u);
+                commit<CG>(&sm.empty[s]);
+                if (++s == ST) { s = 0; par ^= 1; }
+            }
+            if (ok) commit<CG>(&sm.acc_full[buf]);
+        }
+    }
+}
+
+// An epilogue warp's columns of an accumulator added to v (or taken, from the first chunk).
+template <int H>
+__device__ __forceinline__ void add_columns(uint32_t t, float* v, bool take) {
+    constexpr int CH = H < 16 ? H : 16;
+    #pragma unroll
+    for (int i = 0; i < H / CH; ++i) {
+        uint32_t u[CH];
+        Cols<CH>::load(t + i * CH, u);
+        tmem_wait_ld();
+        #pragma unroll
+        for (int e = 0; e < CH; ++e) v[i * CH + e] = take ? __uint_as_float(u[e]) : v[i * CH + e] + __uint_as_float(u[e]);
+    }
+}
+template <int CG, int ST>
+__device__ __forceinline__ void release(Bars<ST>& sm, int buf, int lane) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+        if (CG == 2) arrive_at(map_to(smem_u32(&sm.acc_empty[buf]), 0));
+        else mbar_arrive(&sm.acc_empty[buf]);
+    }
+}
+
+// ---------------------------------------------------------------- few rows
+// Lanes are columns c of C, accumulator columns its rows.  Grid: a cluster of `split` CTAs per
+// tile of 128 c; the parts of the sum meet in shared memory and are added in rank order.
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 2)
+k_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a) {
+    using F = Cfg<1, BN>;
+    constexpr int ST = F::kStages, H = F::kHalf, E = H < 16 ? H : 16;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Bars<ST> sm;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Work w = work_of<1>(a);
+    const uint32_t tmem = start<1, BN, ST>(sm, warp);
+    int tc, tr;
+    tile_at(a, w.first, tc, tr);
+    if (warp == kEpiWarps) {
+        if (lane == 0) produce<1, BN, false, ST>(&tm_a, &tm_b, a, w, sm, ring);
+    } else if (warp == kEpiWarps + 1) {
+        if (lane == 0) issue<1, BN, ST>(a, w, sm, ring, tmem);
+    } else {
         const int q = warp & 3, half = warp >> 2;
         const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + half * H;
-        int ac = 0;
+        float v[H];
         bool ok = true;
-        for (int t = first; ok && t < ntiles; t += step) {
-            int tc, tr;
-            tile_at(t, tc, tr);
-            float v[H];
-            for (int ch = 0; ch < nch; ++ch, ++ac) {
-                const int buf = ac & 1;
-                const bool last = ch == nch - 1;
-                if (!__all_sync(0xffffffffu, mbar_wait_inline(&acc_full[buf], (ac / 2) & 1, a.err, 3301))) { ok = false; break; }
-                tc_fence_after();
-                if (nch > 1 || (CG == 1 && a.split > 1)) {
-                    #pragma unroll
-                    for (int i = 0; i < H / CH; ++i) {
-                        uint32_t u[CH];
-                        Cols<CH>::load(at0 + buf * BR + i * CH, u);
-                        tmem_wait_ld();
-                        #pragma unroll
-                        for (int e = 0; e < CH; ++e)
-                            v[i * CH + e] = ch == 0 ? __uint_as_float(u[e]) : v[i * CH + e] + __uint_as_float(u[e]);
-                    }
-                }
-                if (last) {
-                    if (CG == 1 && a.split > 1) {
-                        // the parts meet in shared memory, column j of the tile at part[j][c].  The stages'
-                        // memory is free: this tile is the block's only one and its last product is done.
-                        float* part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));
-                        #pragma unroll
-                        for (int e = 0; e < H; ++e) part[(half * H + e) * 128 + q * 32 + lane] = v[e];
-                    } else {
-                        if (nch > 1) {
-                            #pragma unroll
-                            for (int i = 0; i < H / CH; ++i) Cols<CH>::store(at0 + buf * BR + i * CH, v + i * CH);
-                            tmem_wait_st();
-                        }
-                        const Lane l = lane_of(a, tc * 128 * CG + (CG == 2 ? 128 * (int)rank : 0) + q * 32 + lane);
-                        const int64_t r0 = (int64_t)tr * BR + half * H;
-                        #pragma unroll 1
-                        for (int e = 0; e < H; e += E) {
-                            const int64_t left = a.R - (r0 + e);
-                            if (left <= 0) break;
-                            uint32_t u[E];
-                            Cols<E>::load(at0 + buf * BR + e, u);
-                            tmem_wait_ld();
-                            emit<E>(a, l, r0 + e, left < E ? (int)left : E, u);
-                            __syncwarp();
-                        }
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2) arrive_at(map_to(smem_u32(&acc_empty[buf]), 0));
-                    else mbar_arrive(&acc_empty[buf]);
-                }
+        for (int ch = 0; ch < w.nch; ++ch) {
+            const int buf = ch & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait_inline(&sm.acc_full[buf], (ch / 2) & 1, a.err, 3301))) { ok = false; break; }
+            tc_fence_after();
+            add_columns<H>(at0 + buf * BN, v, ch == 0);
+            release<1>(sm, buf, lane);
+        }
+        if (!ok) {
+            // the status block says so; the results are not complete
+        } else if (a.split > 1) {
+            // column j of the tile at part[j][c].  The stages' memory is free: this tile is the
+            // block's only one and its last product is done.
+            float* part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));
+            #pragma unroll
+            for (int e = 0; e < H; ++e) part[(half * H + e) * 128 + q * 32 + lane] = v[e];
+        } else {
+            const Lane l = lane_of(a, tc * 128 + q * 32 + lane);
+            const int64_t r0 = (int64_t)tr * BN + half * H;
+            #pragma unroll
+            for (int e = 0; e < H; e += E) {
+                const int64_t left = a.R - (r0 + e);
+                if (left > 0) emit<E>(a, l, r0 + e, left < E ? (int)left : E, v + e);
             }
         }
+    }
+    if (a.split > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp < kEpiWarps) {
+            const int c = threadIdx.x & 127;
+            const Lane l = lane_of(a, tc * 128 + c);
+            const int j0 = BN * (int)w.rank / a.split, j1 = BN * ((int)w.rank + 1) / a.split;
+            for (int j = j0 + (threadIdx.x >> 7); j < j1; j += 2) {
+                const int64_t r = (int64_t)tr * BN + j;
+                if (r >= a.R) break;
+                const uint32_t my = ring + (uint32_t)(j * 128 + c) * 4;
+                float s = 0.f;
+                for (int p = 0; p < a.split; ++p) s += ld_peer(map_to(my, p));
+                emit<1>(a, l, r, 1, &s);
+            }
+        }
+        __syncwarp();
+        cluster_sync();                    // no CTA's memory goes while another reads it
+    }
+    finish_cta<1, BN>(tmem, warp);
+}
+
+// ---------------------------------------------------------------- many rows
+// NC results of row r from column c on (bias, kept z, activation, residual), n of them inside C.
+template <int NC>
+__device__ __forceinline__ void finish(const Args& a, float* z, int64_t r, int c, int n) {
+    if (a.bias) {
+        if (n == NC) {
+            if (a.bias_f32) {
+                #pragma unroll
+                for (int i = 0; i < NC; i += 4) {
+                    const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.bias) + c + i));
+                    z[i] += b.x; z[i + 1] += b.y; z[i + 2] += b.z; z[i + 3] += b.w;
+                }
+            } else {
+                #pragma unroll
+                for (int i = 0; i < NC; i += 4) {
+                    const uint2 b = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.bias) + c + i));
+                    z[i] += __uint_as_float(b.x << 16); z[i + 1] += __uint_as_float(b.x & 0xffff0000u);
+                    z[i + 2] += __uint_as_float(b.y << 16); z[i + 3] += __uint_as_float(b.y & 0xffff0000u);
+                }
+            }
+        } else {
+            #pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (i < n) z[i] += a.bias_f32 ? static_cast<const float*>(a.bias)[c + i]
+                                              : __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[c + i]);
+        }
+    }
+    if (a.pre.p && r < a.R) {
+        // the kept z has the operands' 16 bits: the backward forms dz from it for 16-bit products
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.pre.p) + at(a.pre, c) + r * a.pre.rs;
+        if (a.pre.vec && n == NC) {
+            #pragma unroll
+            for (int i = 0; i < NC; i += 4)
+                *reinterpret_cast<uint2*>(p + i) = make_uint2(pack_bf16(z[i], z[i + 1]), pack_bf16(z[i + 2], z[i + 3]));
+        } else {
+            #pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (i < n) p[i] = __float2bfloat16_rn(z[i]);
+        }
+    }
+    switch (a.act) {
+        case PRISM_ACT_GELU:
+            #pragma unroll
+            for (int i = 0; i < NC; ++i) z[i] = act_of(z[i], PRISM_ACT_GELU);
+            break;
+        case PRISM_ACT_GELU_TANH:
+            #pragma unroll
+            for (int i = 0; i < NC; ++i) z[i] = act_of(z[i], PRISM_ACT_GELU_TANH);
+            break;
+        case PRISM_ACT_SILU:
+            #pragma unroll
+            for (int i = 0; i < NC; ++i) z[i] = act_of(z[i], PRISM_ACT_SILU);
+            break;
+        default: break;
+    }
+    if (a.res.p && r < a.R) {
+        if (a.res.f32) {
+            const float* p = static_cast<const float*>(a.res.p) + at(a.res, c) + r * a.res.rs;
+            if (a.res.vec && n == NC) {
+                float4 x[NC / 4];
+                #pragma unroll
+                for (int i = 0; i < NC / 4; ++i) x[i] = reinterpret_cast<const float4*>(p)[i];
+                #pragma unroll
+                for (int i = 0; i < NC / 4; ++i) {
+                    z[4 * i] += x[i].x; z[4 * i + 1] += x[i].y; z[4 * i + 2] += x[i].z; z[4 * i + 3] += x[i].w;
+                }
+            } else {
+                #pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    if (i < n) z[i] += p[i];
+            }
+        } else {
+            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.res.p) + at(a.res, c) + r * a.res.rs;
+            if (a.res.vec && n == NC) {
+                uint2 x[NC / 4];
+                #pragma unroll
+                for (int i = 0; i < NC / 4; ++i) x[i] = reinterpret_cast<const uint2*>(p)[i];
+                #pragma unroll
+                for (int i = 0; i < NC / 4; ++i) {
+                    z[4 * i] += __uint_as_float(x[i].x << 16); z[4 * i + 1] += __uint_as_float(x[i].x & 0xffff0000u);
+                    z[4 * i + 2] += __uint_as_float(x[i].y << 16); z[4 * i + 3] += __uint_as_float(x[i].y & 0xffff0000u);
+                }
+            } else {
+                #pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    if (i < n) z[i] += __bfloat162float(p[i]);
+            }
+        }
+    }
+}
+// The same results stored by the thread itself.
+template <int NC>
+__device__ __forceinline__ void store_row(const Args& a, const float* z, int64_t r, int c, int n) {
+    if (r >= a.R) return;
+    if (a.y.f32) {
+        float* p = static_cast<float*>(a.y.p) + at(a.y, c) + r * a.y.rs;
+        if (a.y.vec && n == NC) {
+            #pragma unroll
+            for (int i = 0; i < NC; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
+        } else {
+            #pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (i < n) p[i] = z[i];
+        }
+    } else {
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.y.p) + at(a.y, c) + r * a.y.rs;
+        if (a.y.vec && n == NC) {
+            #pragma unroll
+            for (int i = 0; i < NC; i += 4)
+                *reinterpret_cast<uint2*>(p + i) = make_uint2(pack_bf16(z[i], z[i + 1]), pack_bf16(z[i + 2], z[i + 3]));
+        } else {
+            #pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (i < n) p[i] = __float2bfloat16_rn(z[i]);
+        }
+    }
+}
+__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 :: "l"(reinterpret_cast<uint64_t>(tmap)), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+constexpr int kStageOut = 4096;            // an epilogue warp's outgoing 32 rows of 128 bytes
+template <int CG, int BN>
+constexpr int tile_smem() { return Cfg<CG, BN>::kRing + kEpiWarps * kStageOut + 1024; }
+constexpr int kPartPitch = 132;            // floats per row of a part (CG 1): rows start 4 banks apart
+
+// Lanes are rows of C.  Grid: pairs (CG 2) walk the tiles; or a cluster of `split` CTAs per tile.
+template <int CG, int BN>
+__global__ void __launch_bounds__(kThreads, CG == 2 ? 1 : 2)
+k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+       const __grid_constant__ CUtensorMap tm_y, const Args a) {
+    using F = Cfg<CG, BN>;
+    constexpr int ST = F::kStages, H = F::kHalf;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Bars<ST> sm;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Work w = work_of<CG>(a);
+    const uint32_t tmem = start<CG, BN, ST>(sm, warp);
+    if (warp == kEpiWarps) {
+        if (lane == 0) produce<CG, BN, true, ST>(&tm_a, &tm_b, a, w, sm, ring);
+    } else if (warp == kEpiWarps + 1) {
+        if (lane == 0 && (CG == 1 || w.rank == 0)) issue<CG, BN, ST>(a, w, sm, ring, tmem);
+    } else {
+        const int q = warp & 3, half = warp >> 2;
+        const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + half * H;
+        const uint32_t stage = ring + F::kRing + warp * kStageOut;
+        const bool parts = CG == 1 && a.split > 1;
+        int ac = 0;
+        bool ok = true;
+        for (int t = w.first; ok && t < w.ntiles; t += w.step) {
+            int tc, tr;
+            tile_at(a, t, tc, tr);
+            const int64_t r0 = (int64_t)tr * F::kM + (CG == 2 ? 128 * (int)w.rank : 0) + q * 32;
+            const int c0 = tc * BN + half * H;
+            int buf = ac & 1;
+            if (w.nch > 1 || parts) {
+                // the chunks add up in registers; the sum goes back to the last one's columns
+                float v[H];
+                for (int ch = 0; ch < w.nch; ++ch, ++ac) {
+                    buf = ac & 1;
+                    if (!__all_sync(0xffffffffu, mbar_wait_inline(&sm.acc_full[buf], (ac / 2) & 1, a.err, 3301))) { ok = false; break; }
+                    tc_fence_after();
+                    add_columns<H>(at0 + buf * BN, v, ch == 0);
+                    if (ch < w.nch - 1) release<CG>(sm, buf, lane);
+                }
+                if (!ok) break;
+                if (parts) {
+                    // row by row into the stages' memory, free since this tile is the block's only one
+                    float* part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));
+                    #pragma unroll
+                    for (int e = 0; e < H; e += 4)
+                        *reinterpret_cast<float4*>(part + (q * 32 + lane) * kPartPitch + half * H + e) =
+                            make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    release<CG>(sm, buf, lane);
+                    break;
+                }
+                #pragma unroll
+                for (int i = 0; i < H / 8; ++i) Cols<8>::store(at0 + buf * BN + i * 8, v + i * 8);
+                tmem_wait_st();
+            } else {
+                if (!__all_sync(0xffffffffu, mbar_wait_inline(&sm.acc_full[buf], (ac / 2) & 1, a.err, 3301))) { ok = false; break; }
+                tc_fence_after();
+                ++ac;
+            }
+            #pragma unroll 1
+            for (int e = 0; e < H; e += 32) {
+                const int c = c0 + e, n = min(32, a.C - c);
+                if (n <= 0) break;
+                uint32_t u[32];
+                PRISM_TMEM_LD32(at0 + buf * BN + e, u);
+                tmem_wait_ld();
+                float z[32];
+                #pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
+                finish<32>(a, z, r0 + lane, c, n);
+                if (a.y_tma) {
+                    // 32 columns are a whole 128-byte row of the stage in fp32, half of one in bf16
+                    const bool begin = a.y.f32 || !(e & 32), end = a.y.f32 || (e & 32) || e + 32 >= H || c + 32 >= a.C;
+                    if (begin) {
+                        if (lane == 0) bulk_wait_read0();      // the stage's last store has read it
+                        __syncwarp();
+                    }
+                    if (a.y.f32) {
+                        #pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            st_shared_v4(stage + swz128(lane, k), __float_as_uint(z[4 * k]), __float_as_uint(z[4 * k + 1]),
+                                         __float_as_uint(z[4 * k + 2]), __float_as_uint(z[4 * k + 3]));
+                    } else {
+                        #pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            st_shared_v4(stage + swz128(lane, (e & 32) / 8 + k), pack_bf16(z[8 * k], z[8 * k + 1]),
+                                         pack_bf16(z[8 * k + 2], z[8 * k + 3]), pack_bf16(z[8 * k + 4], z[8 * k + 5]),
+                                         pack_bf16(z[8 * k + 6], z[8 * k + 7]));
+                    }
+                    if (end) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            // what lies outside C is not written
+                            const int cs = a.y.f32 ? c : c & ~63;
+                            const int zh = a.y.hd ? cs / a.y.hd : 0;
+                            tma_store_3d(&tm_y, stage, cs - zh * a.y.hd, (int)r0, zh);
+                            bulk_commit();
+                        }
+                    }
+                } else {
+                    store_row<32>(a, z, r0 + lane, c, n);
+                }
+                __syncwarp();
+            }
+            release<CG>(sm, buf, lane);
+        }
+        if (lane == 0) bulk_wait0();
     }
     if (CG == 1 && a.split > 1) {
         __syncwarp();
         cluster_sync();
-        // each CTA of the cluster sums its share of the columns over the parts, in rank order
+        // each CTA of the cluster finishes its share of the rows, the parts added in rank order
         if (warp < kEpiWarps) {
             int tc, tr;
-            tile_at(first, tc, tr);
-            const int c = threadIdx.x & 127;
-            const Lane l = lane_of(a, tc * 128 + c);
-            const int j0 = BR * (int)rank / a.split, j1 = BR * ((int)rank + 1) / a.split;
-            for (int j = j0 + (threadIdx.x >> 7); j < j1; j += 2) {
-                const uint32_t my = ring + (uint32_t)(j * 128 + c) * 4;
-                float s = 0.f;
-                for (int p = 0; p < a.split; ++p) s += ld_peer(map_to(my, p));
-                const int64_t r = (int64_t)tr * BR + j;
-                const uint32_t u = __float_as_uint(s);
-                if (r < a.R) emit<1>(a, l, r, 1, &u);
+            tile_at(a, w.first, tc, tr);
+            const int j0 = 128 * (int)w.rank / a.split, j1 = 128 * ((int)w.rank + 1) / a.split;
+            const int c = tc * BN + lane * 4, n = min(4, a.C - c);
+            for (int j = j0 + warp; j < j1; j += kEpiWarps) {
+                const int64_t r = (int64_t)tr * 128 + j;
+                if (r >= a.R || n <= 0) continue;
+                const uint32_t my = ring + (uint32_t)(j * kPartPitch + lane * 4) * 4;
+                float z[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int p = 0; p < a.split; ++p) {
+                    const float4 x = ld_peer4(map_to(my, p));
+                    z[0] += x.x; z[1] += x.y; z[2] += x.z; z[3] += x.w;
+                }
+                finish<4>(a, z, r, c, n);
+                store_row<4>(a, z, r, c, n);
             }
         }
         __syncwarp();
-        cluster_sync();                      // no CTA's memory goes while another reads it
+        cluster_sync();                    // no CTA's memory goes while another reads it
     }
-    tc_fence_before();
-    __syncwarp();
-    if (CG == 2) cluster_sync();
-    else __syncthreads();
-    tc_fence_after();
-    if (warp == W_PROD) {
-        __syncwarp();
-        free_tmem<CG>(tmem, F::kCols);
-    }
+    finish_cta<CG, BN>(tmem, warp);
 }
 
 // ------------------------------------------------- elementwise passes
@@ -661,41 +965,53 @@ static int make_map(CUtensorMap* m, const Matrix& x, int box) {
     return r == CUDA_SUCCESS ? PRISM_OK : PRISM_ERR_CUDA;
 }
 
-struct Shape {
-    int cg, br, split;
-};
+// C as boxes of 32 rows by 128 bytes.
+static int make_out_map(CUtensorMap* m, const Out& y, int64_t R, int C) {
+    auto enc = encode_fn();
+    if (!enc) return PRISM_ERR_CUDA;
+    const int e = y.f32 ? 4 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)(y.hd ? y.hd : C), (cuuint64_t)R, (cuuint64_t)(y.hd ? C / y.hd : 1)};
+    cuuint64_t strides[2] = {(cuuint64_t)y.rs * e, (cuuint64_t)(y.hd ? y.hs : R * y.rs) * e};
+    cuuint32_t boxd[3] = {(cuuint32_t)(128 / e), 32, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    CUresult r = enc(m, y.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, y.p, dims, strides,
+                     boxd, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PRISM_OK : PRISM_ERR_CUDA;
+}
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+struct Shape {
+    int few;                               // k_few, else k_tile
+    int cg, bn, split;
+};
+
 // The tile of a product of R rows, C columns and kb stages.
-static Shape shape_of(int64_t R, int64_t C, int kb, bool b_mn) {
-    const int64_t pairs = ceil_div(R, 256) * ceil_div(C, 256);
-    if (R > 128 && pairs >= 74) return Shape{2, 256, 1};
-    Shape s{1, 128, 1};
-    for (int br : {16, 32, 64})
-        if (R <= br && !(b_mn && br < 64)) { s.br = br; break; }
-    const int64_t tiles = ceil_div(R, s.br) * ceil_div(C, 128);
+static Shape shape_of(int64_t R, int64_t C, int kb, bool x_mn) {
+    if (R <= 64) {
+        Shape s{1, 1, 64, 1};
+        if (!x_mn) s.bn = R <= 16 ? 16 : R <= 32 ? 32 : 64;      // an MN-major slab has 64 rows
+        const int64_t tiles = ceil_div(C, 128);
+        while (s.split < 8 && tiles * s.split * 2 <= 2 * 148 && kb >= 8 * s.split) s.split *= 2;
+        return s;
+    }
+    if (ceil_div(R, 256) * ceil_div(C, 256) >= 74) return Shape{0, 2, 256, 1};
+    Shape s{0, 1, 128, 1};
+    const int64_t tiles = ceil_div(R, 128) * ceil_div(C, 128);
     while (s.split < 8 && tiles * s.split * 2 <= 2 * 148 && kb >= 8 * s.split) s.split *= 2;
     return s;
 }
 
-template <int CG, int BR>
-static int launch(const CUtensorMap& ta, const CUtensorMap& tb, Args& a, int split, cudaStream_t s) {
-    using F = Cfg<CG, BR>;
-    a.split = split;
-    a.tiles_c = (int)ceil_div(a.C, 128 * CG);
-    const int64_t tr = ceil_div(a.R, BR);
-    if (tr * a.tiles_c > 0x3fffffff) return PRISM_ERR_INVALID_ARG;
-    a.tiles_r = (int)tr;
-    a.band = 8;
-    const int64_t tiles = tr * a.tiles_c;
-    if (cudaFuncSetAttribute(k_gemm<CG, BR>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) != cudaSuccess)
-        return PRISM_ERR_CUDA;
+// Starts `kernel` as clusters of `group` CTAs.  The shared-memory opt-in is made for every call:
+// it belongs to the device that is current.
+template <typename... P, typename... A>
+static int start_kernel(void (*kernel)(P...), int64_t ctas, int group, int smem, cudaStream_t s, const A&... args) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return PRISM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    const int group = CG == 2 ? 2 : split;
-    cfg.gridDim = dim3((unsigned)(CG == 2 ? 2 * (tiles < 74 ? tiles : 74) : tiles * split));
+    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = F::kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -704,31 +1020,54 @@ static int launch(const CUtensorMap& ta, const CUtensorMap& tb, Args& a, int spl
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_gemm<CG, BR>, ta, tb, a) == cudaSuccess ? PRISM_OK : PRISM_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? PRISM_OK : PRISM_ERR_CUDA;
 }
 
-// C[r][c] = sum_k B[r][k] A[c][k]; K the contraction's length, a_mn / b_mn: the matrix's rows are k.
-static int product(const Matrix& A, bool a_mn, const Matrix& B, bool b_mn, int64_t R, int C, int64_t K, Args& a,
+template <int CG, int BN>
+static int launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty, const Args& a, cudaStream_t s) {
+    const int64_t tiles = (int64_t)a.tiles_c * a.tiles_r;
+    return start_kernel(k_tile<CG, BN>, CG == 2 ? 2 * (tiles < 74 ? tiles : 74) : tiles * a.split, CG == 2 ? 2 : a.split,
+                        tile_smem<CG, BN>(), s, ta, tb, ty, a);
+}
+template <int BN>
+static int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const Args& a, cudaStream_t s) {
+    return start_kernel(k_few<BN>, (int64_t)a.tiles_c * a.tiles_r * a.split, a.split, Cfg<1, BN>::kRing + 1024, s, ta, tb, a);
+}
+
+static Operand operand_of(const Matrix& m, bool mn) { return Operand{m.heads > 1 ? (int)m.inner : 0, mn}; }
+
+// C[r][c] = sum_k X[r][k] Y[c][k]; K the contraction's length, x_mn / y_mn: the matrix's rows are k.
+static int product(const Matrix& X, bool x_mn, const Matrix& Y, bool y_mn, int64_t R, int C, int64_t K, Args& a,
                    cudaStream_t s) {
     a.R = R;
     a.C = C;
     a.kblocks = (int)ceil_div(K, kKB);
-    a.a.mn = a_mn;
-    a.b.mn = b_mn;
-    a.a.inner = A.heads > 1 ? (int)A.inner : 0x7fffffff;
-    a.b.inner = B.heads > 1 ? (int)B.inner : 0x7fffffff;
-    const Shape sh = shape_of(R, C, a.kblocks, b_mn);
-    CUtensorMap ta, tb;
-    int st = make_map(&ta, A, a_mn ? kKB : 128);
-    if (!st) st = make_map(&tb, B, b_mn ? kKB : sh.br / sh.cg);
+    const Shape sh = shape_of(R, C, a.kblocks, x_mn);
+    a.split = sh.split;
+    a.chunk = a.y.f32 ? kChunkF32 : kChunkBF16;
+    a.band = 8;
+    const int rows = sh.few ? sh.bn : 128 * sh.cg, cols = sh.few ? 128 : sh.bn;
+    const int64_t tr = ceil_div(R, rows), tc = ceil_div(C, cols);
+    if (tr * tc > 0x0fffffff) return PRISM_ERR_INVALID_ARG;
+    a.tiles_r = (int)tr;
+    a.tiles_c = (int)tc;
+    CUtensorMap tx, ty;
+    int st = make_map(&tx, X, x_mn ? kKB : sh.few ? sh.bn : 128);
+    if (!st) st = make_map(&ty, Y, y_mn ? kKB : sh.few ? 128 : sh.bn / sh.cg);
     if (st) return st;
-    if (sh.cg == 2) return launch<2, 256>(ta, tb, a, 1, s);
-    switch (sh.br) {
-        case 16: return launch<1, 16>(ta, tb, a, sh.split, s);
-        case 32: return launch<1, 32>(ta, tb, a, sh.split, s);
-        case 64: return launch<1, 64>(ta, tb, a, sh.split, s);
-        default: return launch<1, 128>(ta, tb, a, sh.split, s);
+    if (sh.few) {
+        a.a = operand_of(Y, y_mn);
+        a.b = operand_of(X, x_mn);
+        return sh.bn == 16 ? launch_few<16>(ty, tx, a, s) : sh.bn == 32 ? launch_few<32>(ty, tx, a, s) : launch_few<64>(ty, tx, a, s);
     }
+    a.a = operand_of(X, x_mn);
+    a.b = operand_of(Y, y_mn);
+    // a map of C wants its address and row stride in whole 16 bytes
+    CUtensorMap to{};
+    a.y_tma = a.y.vec;
+    if (a.y_tma) st = make_out_map(&to, a.y, R, C);
+    if (st) return st;
+    return sh.cg == 2 ? launch_tile<2, 256>(tx, ty, to, a, s) : launch_tile<1, 128>(tx, ty, to, a, s);
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -789,6 +1128,7 @@ static Out out_rows(const void* p, int64_t M, int N, int heads, int64_t stride, 
     o.hd = heads ? N / heads : 0;
     o.rs = heads ? o.hd : stride;
     o.hs = heads ? M * (int64_t)o.hd : 0;
+    o.vec = o.rs * (f32 ? 4 : 2) % 16 == 0;
     return o;
 }
 
@@ -858,7 +1198,7 @@ static int forward(const prism_linear_params* p, const void* x, const void* W, c
     a.bias_f32 = p->bias_dtype == PRISM_F32;
     a.act = p->activation;
     a.err = err;
-    return product(mw, false, mx, false, p->M, p->N, p->K, a, s);
+    return product(mx, false, mw, false, p->M, p->N, p->K, a, s);
 }
 
 static int backward(const prism_linear_params* p, const void* dy, const void* x, const void* W, const void* pre, void* dx,
@@ -894,7 +1234,7 @@ static int backward(const prism_linear_params* p, const void* dy, const void* x,
         Args a{};
         a.y = out_rows(dx, p->M, p->K, p->in_heads, p->K, 0);
         a.err = err;
-        st = product(mw, true, mz, false, p->M, p->K, p->N, a, s);
+        st = product(mz, false, mw, true, p->M, p->K, p->N, a, s);
         if (st) return st;
     }
     if (dW) {
@@ -903,7 +1243,7 @@ static int backward(const prism_linear_params* p, const void* dy, const void* x,
         Args a{};
         a.y = out_rows(dW, p->N, p->K, 0, p->K, p->dw_dtype == PRISM_F32);
         a.err = err;
-        st = product(mx, true, mz, true, p->N, p->K, p->M, a, s);
+        st = product(mz, true, mx, true, p->N, p->K, p->M, a, s);
     }
     return st;
 }

@@ -5,9 +5,13 @@ Exactness: with small-integer operands every product and every partial sum is an
 without an activation the stored result is the exact value rounded once.
 
 With an activation, z is exact and act(z) is a few fp32 operations on it: CUDA documents erff
-within 2 ulp, expf 2, tanhf 2, division 0 beyond rounding.  Each form is 0.5 z (1 + f) or
-z / (1 + e): |error| <= 16 EPS32 (|z| + 1) covers the argument's 4 roundings (amplified by at most
-|z| f' <= 1) and the result's; its derivative likewise is within 32 EPS32 (|z| + 1)."""
+within 2 ulp, __expf(t) within 2 + 1.173 |t| ulp, __fdividef within 2 ulp.  0.5 z (1 + erf) is then
+within 16 EPS32 (|z| + 1), the argument's roundings amplified by at most |z| f' <= 1 included.
+z s with s = 1 / (1 + e^-t): e's relative error 2 EPS32 (2 + 1.173 |t|) and the argument's 4 roundings
+(4 |t| EPS32) reach s by the factor s (1 - s), and s (1 - s) |t| < 0.23, s (1 - s) <= 0.25: at most
+(1 + 0.6 + 0.9) EPS32, the quotient adds 4 EPS32 s and the product 1: within 16 EPS32 (|z| + 1).
+The derivative s + z s (1 - s) t' has |z t'| s (1 - s) < 2 and multiplies one more such s: within
+32 EPS32 (|z| + 1)."""
 import math
 
 import torch
