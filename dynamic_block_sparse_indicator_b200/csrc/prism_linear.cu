@@ -6,15 +6,16 @@
 // prism_attn_fwd writes, without a transposing copy.
 //
 // Every product is C[r][c] = sum_k X[r][k] Y[c][k], c the contiguous index of C.  An operand
-// is a 3-D TMA map (inner, rows, heads) with the contraction along the inner index (K-major)
-// or along the rows (MN-major); head-major inner coordinates split into (channel, head):
+// is a TMA map (inner, rows, heads) with the contraction along the inner index (K-major) or
+// along the rows (MN-major); head-major inner coordinates split into (channel, head):
 //     forward  X = x  [M][K] K-major     Y = W [N][K] K-major
 //     dx       X = dz [M][N] K-major     Y = W [N][K] MN-major
 //     dW       X = dz [M][N] MN-major    Y = x [M][K] MN-major
 // Two kernels:
 //   k_tile  many rows: TMEM lanes are rows, columns are c.  A pair of CTAs (cta_group::2)
 //           shares a 256 x BN tile, or one CTA has 128 x 128, whose contraction a cluster may
-//           split.  A warp's results leave through a 4 KB stage and TMA stores.
+//           split.  A pair's results leave through 4 KB stages and TMA stores; a single CTA's
+//           straight from the registers (two CTAs on an SM leave no room for stages).
 //   k_few   up to 64 rows: TMEM lanes are c and columns are rows, so few tokens are a small
 //           N of the instruction instead of an M tile of padding.  Bound by HBM's read of W;
 //           a cluster splits the contraction.
@@ -49,8 +50,9 @@ constexpr int kChunkF32 = 32;              // stages per accumulation chunk (see
 constexpr int kChunkBF16 = 256;            // and 16,384 where the result keeps 16 bits
 
 struct Operand {
-    int inner;                             // extent of the inner index of one head
-    int mn;                                // 1 = MN-major
+    int mn;                                // MN-major
+    int shift;                             // K-major: k >> shift is the head, the rest the channel (31: one head)
+    int slabs;                             // MN-major: slabs of 64 before the next head; 0: no whole slabs
 };
 
 struct Out {
@@ -78,16 +80,16 @@ struct Args {
 
 // ---------------------------------------------------------------- PTX
 template <int CG>
-__device__ __forceinline__ void tma3(uint32_t dst, const void* tmap, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+__device__ __forceinline__ void tma4(uint32_t dst, const void* tmap, uint32_t bar, int32_t x, int32_t y, int32_t z, int32_t v) {
     if (CG == 2)
         // the barrier may lie in the pair's other CTA
-        asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-                     " [%0], [%1, {%3, %4, %5}], [%2];"
-                     :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+        asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+                     :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(v) : "memory");
     else
-        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                     " [%0], [%1, {%3, %4, %5}], [%2];"
-                     :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+        asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+                     :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(v) : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -376,20 +378,40 @@ __device__ __forceinline__ void finish_cta(uint32_t tmem, int warp) {
     }
 }
 
-// One operand's part of a stage: ROWS rows of the tile from `o0` on.
+// One operand's tile at the producer: the fixed coordinates of its copies.  K-major: one box of
+// ROWS rows by 64 k.  MN-major: 64 k by slabs of 64 columns, one box of every slab where the
+// map has a slab dimension, else a box each.
 template <int CG, int ROWS>
-__device__ __forceinline__ void load_operand(uint32_t dst, const void* tm, uint32_t bar, const Operand& o, int o0, int k) {
-    if (o.mn) {
-        #pragma unroll
-        for (int i = 0; i < (ROWS + 63) / 64; ++i) {
-            const int c = o0 + 64 * i, z = o.inner ? c / o.inner : 0;
-            tma3<CG>(dst + i * 8192, tm, bar, c - z * o.inner, k, z);
-        }
-    } else {
-        const int z = o.inner ? k / o.inner : 0;
-        tma3<CG>(dst, tm, bar, k - z * o.inner, o0, z);
+struct Feed {
+    const void* tm;
+    int mn, shift, mask, two, x0, y0, z0, v0;
+    __device__ __forceinline__ Feed(const void* tm, const Operand& o) : tm(tm), mn(o.mn), shift(o.shift) {
+        mask = o.shift == 31 ? 0x7fffffff : (1 << o.shift) - 1;
+        two = o.mn && !o.slabs && ROWS > 64;
+        x0 = y0 = z0 = v0 = 0;
     }
-}
+    __device__ __forceinline__ void tile(const Operand& o, int o0) {
+        if (!mn) {
+            y0 = o0;
+        } else if (o.slabs) {
+            const int sl = o0 >> 6;
+            v0 = sl / o.slabs;
+            z0 = sl - v0 * o.slabs;
+        } else {
+            x0 = o0;
+        }
+    }
+    __device__ __forceinline__ void load(uint32_t dst, uint32_t bar, int k) const {
+        const int x = mn ? x0 : k & mask, y = mn ? k : y0, z = mn ? z0 : k >> shift;
+        tma4<CG>(dst, tm, bar, x, y, z, v0);
+        if (two) tma4<CG>(dst + 8192, tm, bar, x + 64, y, z, v0);
+    }
+};
+
+// The two issuing loops run once per 64 of k beside products of 512 cycles, each in one thread:
+// their instructions are a latency chain (with divisions, address maps and constants reloaded in
+// the loop the producer took 626 to 780 cycles per stage and bound the products).  So all that
+// is fixed is in registers before the loop.
 
 // The TMA producer (one thread).  ROWS_ARE_M: C's rows lie along the tensor core's M.
 template <int CG, int BN, bool ROWS_ARE_M, int ST>
@@ -398,22 +420,26 @@ __device__ __forceinline__ void produce(const void* tm_a, const void* tm_b, cons
     using F = Cfg<CG, BN>;
     tma_prefetch_desc(tm_a);
     tma_prefetch_desc(tm_b);
+    Feed<CG, 128> fa(tm_a, a.a);
+    Feed<CG, BN / CG> fb(tm_b, a.b);
+    // the pair's first CTA has the barrier of both CTAs' copies and expects their bytes
+    const uint32_t bars = CG == 2 ? map_to(smem_u32(sm.full), 0) : smem_u32(sm.full);
+    const bool expects = CG == 1 || w.rank == 0;
+    int* const err = a.err;
     int s = 0, round = 0;
     bool ok = true;
     for (int t = w.first; ok && t < w.ntiles; t += w.step) {
         int tc, tr;
         tile_at(a, t, tc, tr);
-        const int m0 = (ROWS_ARE_M ? tr : tc) * F::kM + (CG == 2 ? 128 * (int)w.rank : 0);
-        const int n0 = (ROWS_ARE_M ? tc : tr) * BN + (CG == 2 ? (BN / 2) * (int)w.rank : 0);
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
-            if (round && !mbar_wait(&sm.empty[s], (round - 1) & 1, a.err, 3101)) { ok = false; break; }
-            uint32_t bar = smem_u32(&sm.full[s]);
-            if (CG == 2) bar = map_to(bar, 0);
-            // the pair's first CTA expects the bytes of both
-            if (CG == 1 || w.rank == 0) mbar_expect_tx(&sm.full[s], CG * F::kStage);
-            const uint32_t da = ring + s * F::kStage;
-            load_operand<CG, 128>(da, tm_a, bar, a.a, m0, kb * kKB);
-            load_operand<CG, BN / CG>(da + F::kA, tm_b, bar, a.b, n0, kb * kKB);
+        fa.tile(a.a, (ROWS_ARE_M ? tr : tc) * F::kM + (CG == 2 ? 128 * (int)w.rank : 0));
+        fb.tile(a.b, (ROWS_ARE_M ? tc : tr) * BN + (CG == 2 ? (BN / 2) * (int)w.rank : 0));
+        const int k1 = w.kb1 * kKB;
+        for (int k = w.kb0 * kKB; k < k1; k += kKB) {
+            if (round && !mbar_wait(&sm.empty[s], (round - 1) & 1, err, 3101)) { ok = false; break; }
+            if (expects) mbar_expect_tx(&sm.full[s], CG * F::kStage);
+            const uint32_t da = ring + s * F::kStage, bar = bars + s * 8;
+            fa.load(da, bar, k);
+            fb.load(da + F::kA, bar, k);
             if (++s == ST) { s = 0; ++round; }
         }
     }
@@ -431,23 +457,24 @@ __device__ __forceinline__ void issue(const Args& a, const Work& w, Bars<ST>& sm
     using F = Cfg<CG, BN>;
     const uint32_t idesc = idesc_bf16(128 * CG, BN, a.a.mn, a.b.mn);
     const uint32_t sa = a.a.mn ? 128 : 2, sb = a.b.mn ? 128 : 2;        // 16-byte units per 16 of k
-    const uint32_t la = a.a.mn ? 8192 : 16, lb = a.b.mn ? 8192 : 16;
+    const uint32_t da0 = desc_lo(ring, a.a.mn ? 8192 : 16), db0 = desc_lo(ring + F::kA, a.b.mn ? 8192 : 16);
+    int* const err = a.err;
     int s = 0, par = 0, ac = 0;
     bool ok = true;
     for (int t = w.first; ok && t < w.ntiles; t += w.step) {
         for (int ch = 0; ok && ch < w.nch; ++ch, ++ac) {
             const int n = (int)((int64_t)w.nk * (ch + 1) / w.nch - (int64_t)w.nk * ch / w.nch), buf = ac & 1;
-            if (ac >= 2 && !mbar_wait(&sm.acc_empty[buf], (ac / 2 - 1) & 1, a.err, 3201)) { ok = false; break; }
+            if (ac >= 2 && !mbar_wait(&sm.acc_empty[buf], (ac / 2 - 1) & 1, err, 3201)) { ok = false; break; }
             tc_fence_after();
+            const uint32_t acc = tmem + buf * BN;
             for (int i = 0; i < n; ++i) {
-                if (!mbar_wait(&sm.full[s], par, a.err, 3202)) { ok = false; break; }
+                if (!mbar_wait(&sm.full[s], par, err, 3202)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t da = desc_lo(ring + s * F::kStage, la);
-                const uint32_t db = desc_lo(ring + s * F::kStage + F::kA, lb);
+                const uint32_t da = da0 + s * (F::kStage >> 4), db = db0 + s * (F::kStage >> 4);
+                mma<CG>(acc, desc_from_lo(da), desc_from_lo(db), idesc, i > 0 ? 1u : 0u);
                 #pragma unroll
-                for (int kk = 0; kk < kKB / 16; ++kk)
-                    mma<CG>(tmem + buf * BN, desc_from_lo(da + kk * sa), desc_from_lo(db + kk * sb), idesc,
-                            i > 0 || kk > 0 ? 1u : 0u);
+                for (int kk = 1; kk < kKB / 16; ++kk)
+                    mma<CG>(acc, desc_from_lo(da + kk * sa), desc_from_lo(db + kk * sb), idesc, 1u);
                 commit<CG>(&sm.empty[s]);
                 if (++s == ST) { s = 0; par ^= 1; }
             }
@@ -681,7 +708,7 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t cluster_addr) {
 
 constexpr int kStageOut = 4096;            // an epilogue warp's outgoing 32 rows of 128 bytes
 template <int CG, int BN>
-constexpr int tile_smem() { return Cfg<CG, BN>::kRing + kEpiWarps * kStageOut + 1024; }
+constexpr int tile_smem() { return Cfg<CG, BN>::kRing + (CG == 2 ? kEpiWarps * kStageOut : 0) + 1024; }
 constexpr int kPartPitch = 132;            // floats per row of a part (CG 1): rows start 4 banks apart
 
 // Lanes are rows of C.  Grid: pairs (CG 2) walk the tiles; or a cluster of `split` CTAs per tile.
@@ -754,7 +781,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
                 finish<32>(a, z, r0 + lane, c, n);
-                if (a.y_tma) {
+                if (CG == 2 && a.y_tma) {
                     // 32 columns are a whole 128-byte row of the stage in fp32, half of one in bf16
                     const bool begin = a.y.f32 || !(e & 32), end = a.y.f32 || (e & 32) || e + 32 >= H || c + 32 >= a.C;
                     if (begin) {
@@ -791,7 +818,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
             }
             release<CG>(sm, buf, lane);
         }
-        if (lane == 0) bulk_wait0();
+        if (CG == 2 && lane == 0) bulk_wait0();
     }
     if (CG == 1 && a.split > 1) {
         __syncwarp();
@@ -951,17 +978,33 @@ struct Matrix {
     int heads;
 };
 
-// Boxes of 64 inner elements (128-byte swizzle) by `box` rows; what lies outside reads as zeros.
-static int make_map(CUtensorMap* m, const Matrix& x, int box) {
+// The map of an operand's tiles of `rows` rows (what lies outside the matrix reads as zeros,
+// 128-byte swizzle), and how the producer addresses it.  K-major: boxes of 64 inner elements by
+// `rows` rows.  MN-major: 64 k by `rows` inner elements in slabs of 64.
+static int make_operand(CUtensorMap* m, Operand* o, const Matrix& x, bool mn, int rows) {
     auto enc = encode_fn();
     if (!enc) return PRISM_ERR_CUDA;
-    cuuint64_t dims[3] = {(cuuint64_t)x.inner, (cuuint64_t)x.rows, (cuuint64_t)x.heads};
-    cuuint64_t strides[2] = {(cuuint64_t)x.ld * 2, (cuuint64_t)(x.rows * x.ld) * 2};
-    cuuint32_t boxd[3] = {64, (cuuint32_t)box, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, boxd, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    o->mn = mn;
+    o->shift = x.heads == 1 ? 31 : x.inner == 64 ? 6 : 7;
+    o->slabs = 0;
+    const cuuint64_t row = (cuuint64_t)x.ld * 2, head = (cuuint64_t)(x.rows * x.ld) * 2;
+    cuuint64_t dims[4] = {(cuuint64_t)x.inner, (cuuint64_t)x.rows, (cuuint64_t)x.heads, 1};
+    cuuint64_t strides[3] = {row, head, head};
+    cuuint32_t box[4] = {64, (cuuint32_t)(mn ? kKB : rows), 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    if (mn && x.inner % 64 == 0) {
+        // (64, rows, slabs, heads); a head of 64 channels is a slab itself
+        const bool flat = x.heads == 1, one = !flat && x.inner == 64;
+        o->slabs = one ? x.heads : (int)(x.inner / 64);
+        dims[0] = 64;
+        dims[2] = (cuuint64_t)o->slabs;
+        dims[3] = (cuuint64_t)(flat || one ? 1 : x.heads);
+        strides[1] = one ? head : 128;
+        box[2] = (cuuint32_t)(rows / 64);
+    }
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(x.p), dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PRISM_OK : PRISM_ERR_CUDA;
 }
 
@@ -1034,8 +1077,6 @@ static int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const Args& 
     return start_kernel(k_few<BN>, (int64_t)a.tiles_c * a.tiles_r * a.split, a.split, Cfg<1, BN>::kRing + 1024, s, ta, tb, a);
 }
 
-static Operand operand_of(const Matrix& m, bool mn) { return Operand{m.heads > 1 ? (int)m.inner : 0, mn}; }
-
 // C[r][c] = sum_k X[r][k] Y[c][k]; K the contraction's length, x_mn / y_mn: the matrix's rows are k.
 static int product(const Matrix& X, bool x_mn, const Matrix& Y, bool y_mn, int64_t R, int C, int64_t K, Args& a,
                    cudaStream_t s) {
@@ -1052,19 +1093,17 @@ static int product(const Matrix& X, bool x_mn, const Matrix& Y, bool y_mn, int64
     a.tiles_r = (int)tr;
     a.tiles_c = (int)tc;
     CUtensorMap tx, ty;
-    int st = make_map(&tx, X, x_mn ? kKB : sh.few ? sh.bn : 128);
-    if (!st) st = make_map(&ty, Y, y_mn ? kKB : sh.few ? 128 : sh.bn / sh.cg);
+    Operand ox, oy;
+    int st = make_operand(&tx, &ox, X, x_mn, sh.few ? sh.bn : 128);
+    if (!st) st = make_operand(&ty, &oy, Y, y_mn, sh.few ? 128 : sh.bn / sh.cg);
     if (st) return st;
-    if (sh.few) {
-        a.a = operand_of(Y, y_mn);
-        a.b = operand_of(X, x_mn);
+    a.a = sh.few ? oy : ox;                // along the tensor core's M
+    a.b = sh.few ? ox : oy;
+    if (sh.few)
         return sh.bn == 16 ? launch_few<16>(ty, tx, a, s) : sh.bn == 32 ? launch_few<32>(ty, tx, a, s) : launch_few<64>(ty, tx, a, s);
-    }
-    a.a = operand_of(X, x_mn);
-    a.b = operand_of(Y, y_mn);
     // a map of C wants its address and row stride in whole 16 bytes
     CUtensorMap to{};
-    a.y_tma = a.y.vec;
+    a.y_tma = sh.cg == 2 && a.y.vec;
     if (a.y_tma) st = make_out_map(&to, a.y, R, C);
     if (st) return st;
     return sh.cg == 2 ? launch_tile<2, 256>(tx, ty, to, a, s) : launch_tile<1, 128>(tx, ty, to, a, s);
