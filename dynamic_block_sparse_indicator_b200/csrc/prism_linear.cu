@@ -148,6 +148,13 @@ __device__ __forceinline__ float ld_peer(uint32_t cluster_addr) {
     return v;
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // mbar_wait with its loop in line: the epilogue waits with a tile's sums in registers, which
 // a call would have to save.
 __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, int* err, int where) {
@@ -164,6 +171,11 @@ __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity,
         err[3] = (int)threadIdx.x;
     }
     return false;
+}
+
+// The same for a whole warp: true in every lane, or false in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err, int where) {
+    return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, err, where));
 }
 
 // Accumulator columns of this thread's lane.
@@ -408,18 +420,23 @@ struct Feed {
     }
 };
 
-// The two issuing loops run once per 64 of k beside products of 512 cycles, each in one thread:
-// their instructions are a latency chain (with divisions, address maps and constants reloaded in
-// the loop the producer took 626 to 780 cycles per stage and bound the products).  So all that
-// is fixed is in registers before the loop.
+// The two issuing loops run once per 64 of k, beside products of 256 to 512 cycles, and their
+// instructions are a latency chain: with divisions, address maps and constants reloaded in the
+// loop the producer took 626 to 780 cycles per stage and bound the products.  So what is fixed
+// is in registers before the loop, and the whole warp runs it on values that are the same in
+// every lane, one elected lane only issuing: copies and products take their operands from the
+// warp's uniform registers, which a branch of one lane has to fill one by one.
 
-// The TMA producer (one thread).  ROWS_ARE_M: C's rows lie along the tensor core's M.
+// The TMA producer (one warp).  ROWS_ARE_M: C's rows lie along the tensor core's M.
 template <int CG, int BN, bool ROWS_ARE_M, int ST>
 __device__ __forceinline__ void produce(const void* tm_a, const void* tm_b, const Args& a, const Work& w, Bars<ST>& sm,
                                         uint32_t ring) {
     using F = Cfg<CG, BN>;
-    tma_prefetch_desc(tm_a);
-    tma_prefetch_desc(tm_b);
+    if (elect()) {
+        tma_prefetch_desc(tm_a);
+        tma_prefetch_desc(tm_b);
+    }
+    __syncwarp();
     Feed<CG, 128> fa(tm_a, a.a);
     Feed<CG, BN / CG> fb(tm_b, a.b);
     // the pair's first CTA has the barrier of both CTAs' copies and expects their bytes
@@ -435,11 +452,14 @@ __device__ __forceinline__ void produce(const void* tm_a, const void* tm_b, cons
         fb.tile(a.b, (ROWS_ARE_M ? tc : tr) * BN + (CG == 2 ? (BN / 2) * (int)w.rank : 0));
         const int k1 = w.kb1 * kKB;
         for (int k = w.kb0 * kKB; k < k1; k += kKB) {
-            if (round && !mbar_wait(&sm.empty[s], (round - 1) & 1, err, 3101)) { ok = false; break; }
-            if (expects) mbar_expect_tx(&sm.full[s], CG * F::kStage);
+            if (round && !warp_wait(&sm.empty[s], (round - 1) & 1, err, 3101)) { ok = false; break; }
             const uint32_t da = ring + s * F::kStage, bar = bars + s * 8;
-            fa.load(da, bar, k);
-            fb.load(da + F::kA, bar, k);
+            if (elect()) {
+                if (expects) mbar_expect_tx(&sm.full[s], CG * F::kStage);
+                fa.load(da, bar, k);
+                fb.load(da + F::kA, bar, k);
+            }
+            __syncwarp();
             if (++s == ST) { s = 0; ++round; }
         }
     }
@@ -447,11 +467,11 @@ __device__ __forceinline__ void produce(const void* tm_a, const void* tm_b, cons
     if (CG == 1 || w.rank == 0)
         for (int i = 0; i < ST; ++i) {
             const int uses = round + (i < s ? 1 : 0);
-            if (uses && !mbar_wait(&sm.full[i], (uses - 1) & 1, a.err, 3102)) break;
+            if (uses && !warp_wait(&sm.full[i], (uses - 1) & 1, a.err, 3102)) break;
         }
 }
 
-// The MMA issuer (one thread; of a pair, the first CTA's).
+// The MMA issuer (one warp; of a pair, the first CTA's).
 template <int CG, int BN, int ST>
 __device__ __forceinline__ void issue(const Args& a, const Work& w, Bars<ST>& sm, uint32_t ring, uint32_t tmem) {
     using F = Cfg<CG, BN>;
@@ -464,21 +484,24 @@ __device__ __forceinline__ void issue(const Args& a, const Work& w, Bars<ST>& sm
     for (int t = w.first; ok && t < w.ntiles; t += w.step) {
         for (int ch = 0; ok && ch < w.nch; ++ch, ++ac) {
             const int n = (int)((int64_t)w.nk * (ch + 1) / w.nch - (int64_t)w.nk * ch / w.nch), buf = ac & 1;
-            if (ac >= 2 && !mbar_wait(&sm.acc_empty[buf], (ac / 2 - 1) & 1, err, 3201)) { ok = false; break; }
+            if (ac >= 2 && !warp_wait(&sm.acc_empty[buf], (ac / 2 - 1) & 1, err, 3201)) { ok = false; break; }
             tc_fence_after();
             const uint32_t acc = tmem + buf * BN;
             for (int i = 0; i < n; ++i) {
-                if (!mbar_wait(&sm.full[s], par, err, 3202)) { ok = false; break; }
+                if (!warp_wait(&sm.full[s], par, err, 3202)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t da = da0 + s * (F::kStage >> 4), db = db0 + s * (F::kStage >> 4);
-                mma<CG>(acc, desc_from_lo(da), desc_from_lo(db), idesc, i > 0 ? 1u : 0u);
-                #pragma unroll
-                for (int kk = 1; kk < kKB / 16; ++kk)
-                    mma<CG>(acc, desc_from_lo(da + kk * sa), desc_from_lo(db + kk * sb), idesc, 1u);
-                commit<CG>(&sm.empty[s]);
+                if (elect()) {
+                    mma<CG>(acc, desc_from_lo(da), desc_from_lo(db), idesc, i > 0 ? 1u : 0u);
+                    #pragma unroll
+                    for (int kk = 1; kk < kKB / 16; ++kk)
+                        mma<CG>(acc, desc_from_lo(da + kk * sa), desc_from_lo(db + kk * sb), idesc, 1u);
+                    commit<CG>(&sm.empty[s]);
+                    if (i == n - 1) commit<CG>(&sm.acc_full[buf]);
+                }
+                __syncwarp();
                 if (++s == ST) { s = 0; par ^= 1; }
             }
-            if (ok) commit<CG>(&sm.acc_full[buf]);
         }
     }
 }
@@ -517,15 +540,15 @@ k_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensor
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<ST> sm;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const Work w = work_of<1>(a);
     const uint32_t tmem = start<1, BN, ST>(sm, warp);
     int tc, tr;
     tile_at(a, w.first, tc, tr);
     if (warp == kEpiWarps) {
-        if (lane == 0) produce<1, BN, false, ST>(&tm_a, &tm_b, a, w, sm, ring);
+        produce<1, BN, false, ST>(&tm_a, &tm_b, a, w, sm, ring);
     } else if (warp == kEpiWarps + 1) {
-        if (lane == 0) issue<1, BN, ST>(a, w, sm, ring, tmem);
+        issue<1, BN, ST>(a, w, sm, ring, tmem);
     } else {
         const int q = warp & 3, half = warp >> 2;
         const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + half * H;
@@ -533,7 +556,7 @@ k_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensor
         bool ok = true;
         for (int ch = 0; ch < w.nch; ++ch) {
             const int buf = ch & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait_inline(&sm.acc_full[buf], (ch / 2) & 1, a.err, 3301))) { ok = false; break; }
+            if (!warp_wait(&sm.acc_full[buf], (ch / 2) & 1, a.err, 3301)) { ok = false; break; }
             tc_fence_after();
             add_columns<H>(at0 + buf * BN, v, ch == 0);
             release<1>(sm, buf, lane);
@@ -721,13 +744,13 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<ST> sm;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const Work w = work_of<CG>(a);
     const uint32_t tmem = start<CG, BN, ST>(sm, warp);
     if (warp == kEpiWarps) {
-        if (lane == 0) produce<CG, BN, true, ST>(&tm_a, &tm_b, a, w, sm, ring);
+        produce<CG, BN, true, ST>(&tm_a, &tm_b, a, w, sm, ring);
     } else if (warp == kEpiWarps + 1) {
-        if (lane == 0 && (CG == 1 || w.rank == 0)) issue<CG, BN, ST>(a, w, sm, ring, tmem);
+        if (CG == 1 || w.rank == 0) issue<CG, BN, ST>(a, w, sm, ring, tmem);
     } else {
         const int q = warp & 3, half = warp >> 2;
         const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + half * H;
@@ -746,7 +769,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                 float v[H];
                 for (int ch = 0; ch < w.nch; ++ch, ++ac) {
                     buf = ac & 1;
-                    if (!__all_sync(0xffffffffu, mbar_wait_inline(&sm.acc_full[buf], (ac / 2) & 1, a.err, 3301))) { ok = false; break; }
+                    if (!warp_wait(&sm.acc_full[buf], (ac / 2) & 1, a.err, 3301)) { ok = false; break; }
                     tc_fence_after();
                     add_columns<H>(at0 + buf * BN, v, ch == 0);
                     if (ch < w.nch - 1) release<CG>(sm, buf, lane);
@@ -766,7 +789,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                 for (int i = 0; i < H / 8; ++i) Cols<8>::store(at0 + buf * BN + i * 8, v + i * 8);
                 tmem_wait_st();
             } else {
-                if (!__all_sync(0xffffffffu, mbar_wait_inline(&sm.acc_full[buf], (ac / 2) & 1, a.err, 3301))) { ok = false; break; }
+                if (!warp_wait(&sm.acc_full[buf], (ac / 2) & 1, a.err, 3301)) { ok = false; break; }
                 tc_fence_after();
                 ++ac;
             }
