@@ -15,7 +15,8 @@
 //   k_tile  many rows: TMEM lanes are rows, columns are c.  A pair of CTAs (cta_group::2)
 //           shares a 256 x BN tile, or one CTA has 128 x 128, whose contraction a cluster may
 //           split.  A pair's results leave through 4 KB stages and TMA stores; a single CTA's
-//           straight from the registers (two CTAs on an SM leave no room for stages).
+//           straight from the registers (its shared memory holds a deep ring instead: few CTAs
+//           have to cover the latency).
 //   k_few   up to 64 rows: TMEM lanes are c and columns are rows, so few tokens are a small
 //           N of the instruction instead of an M tile of padding.  Bound by HBM's read of W;
 //           a cluster splits the contraction.
@@ -142,12 +143,6 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ float ld_peer(uint32_t cluster_addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
-    return v;
-}
-
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect() {
     uint32_t p;
@@ -310,9 +305,9 @@ struct Cfg {
     static constexpr int kA = 128 * kKB * 2;                 // bytes of a stage: A, then B
     static constexpr int kB = (BN / CG) * kKB * 2;
     static constexpr int kStage = kA + kB;
-    // CG 2: one CTA per SM; CG 1: two per SM (TMEM 2 x 2 BN <= 512 columns)
-    static constexpr int kStages = (CG == 2 ? 196608 : 98304) / kStage;
-    static constexpr int kCols = 2 * BN;
+    // the pair's CTAs and the single one have an SM to themselves; k_few's run two per SM
+    static constexpr int kStages = (CG == 2 ? 163840 : BN >= 128 ? 196608 : 98304) / kStage;
+    static constexpr int kCols = BN > 128 ? 512 : BN > 64 ? 256 : BN > 32 ? 128 : BN > 16 ? 64 : 32;   // 2 BN, a power of two
     static constexpr int kHalf = BN / 2;                     // columns per epilogue warp
     static constexpr int kRing = kStages * kStage;
 };
@@ -368,7 +363,7 @@ __device__ __forceinline__ uint32_t start(Bars<ST>& sm, int warp) {
     }
     if (warp == kEpiWarps) {
         __syncwarp();
-        alloc_tmem<CG>(&sm.tmem_base, 2 * BN);
+        alloc_tmem<CG>(&sm.tmem_base, Cfg<CG, BN>::kCols);
     }
     tc_fence_before();
     __syncwarp();
@@ -386,7 +381,7 @@ __device__ __forceinline__ void finish_cta(uint32_t tmem, int warp) {
     tc_fence_after();
     if (warp == kEpiWarps) {
         __syncwarp();
-        free_tmem<CG>(tmem, 2 * BN);
+        free_tmem<CG>(tmem, Cfg<CG, BN>::kCols);
     }
 }
 
@@ -529,79 +524,7 @@ __device__ __forceinline__ void release(Bars<ST>& sm, int buf, int lane) {
     }
 }
 
-// ---------------------------------------------------------------- few rows
-// Lanes are columns c of C, accumulator columns its rows.  Grid: a cluster of `split` CTAs per
-// tile of 128 c; the parts of the sum meet in shared memory and are added in rank order.
-template <int BN>
-__global__ void __launch_bounds__(kThreads, 2)
-k_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a) {
-    using F = Cfg<1, BN>;
-    constexpr int ST = F::kStages, H = F::kHalf, E = H < 16 ? H : 16;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ Bars<ST> sm;
-    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    const Work w = work_of<1>(a);
-    const uint32_t tmem = start<1, BN, ST>(sm, warp);
-    int tc, tr;
-    tile_at(a, w.first, tc, tr);
-    if (warp == kEpiWarps) {
-        produce<1, BN, false, ST>(&tm_a, &tm_b, a, w, sm, ring);
-    } else if (warp == kEpiWarps + 1) {
-        issue<1, BN, ST>(a, w, sm, ring, tmem);
-    } else {
-        const int q = warp & 3, half = warp >> 2;
-        const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + half * H;
-        float v[H];
-        bool ok = true;
-        for (int ch = 0; ch < w.nch; ++ch) {
-            const int buf = ch & 1;
-            if (!warp_wait(&sm.acc_full[buf], (ch / 2) & 1, a.err, 3301)) { ok = false; break; }
-            tc_fence_after();
-            add_columns<H>(at0 + buf * BN, v, ch == 0);
-            release<1>(sm, buf, lane);
-        }
-        if (!ok) {
-            // the status block says so; the results are not complete
-        } else if (a.split > 1) {
-            // column j of the tile at part[j][c].  The stages' memory is free: this tile is the
-            // block's only one and its last product is done.
-            float* part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));
-            #pragma unroll
-            for (int e = 0; e < H; ++e) part[(half * H + e) * 128 + q * 32 + lane] = v[e];
-        } else {
-            const Lane l = lane_of(a, tc * 128 + q * 32 + lane);
-            const int64_t r0 = (int64_t)tr * BN + half * H;
-            #pragma unroll
-            for (int e = 0; e < H; e += E) {
-                const int64_t left = a.R - (r0 + e);
-                if (left > 0) emit<E>(a, l, r0 + e, left < E ? (int)left : E, v + e);
-            }
-        }
-    }
-    if (a.split > 1) {
-        __syncwarp();
-        cluster_sync();
-        if (warp < kEpiWarps) {
-            const int c = threadIdx.x & 127;
-            const Lane l = lane_of(a, tc * 128 + c);
-            const int j0 = BN * (int)w.rank / a.split, j1 = BN * ((int)w.rank + 1) / a.split;
-            for (int j = j0 + (threadIdx.x >> 7); j < j1; j += 2) {
-                const int64_t r = (int64_t)tr * BN + j;
-                if (r >= a.R) break;
-                const uint32_t my = ring + (uint32_t)(j * 128 + c) * 4;
-                float s = 0.f;
-                for (int p = 0; p < a.split; ++p) s += ld_peer(map_to(my, p));
-                emit<1>(a, l, r, 1, &s);
-            }
-        }
-        __syncwarp();
-        cluster_sync();                    // no CTA's memory goes while another reads it
-    }
-    finish_cta<1, BN>(tmem, warp);
-}
-
-// ---------------------------------------------------------------- many rows
+// ---------------------------------------------------------------- rows of results
 // NC results of row r from column c on (bias, kept z, activation, residual), n of them inside C.
 template <int NC>
 __device__ __forceinline__ void finish(const Args& a, float* z, int64_t r, int c, int n) {
@@ -718,6 +641,8 @@ __device__ __forceinline__ void store_row(const Args& a, const float* z, int64_t
         }
     }
 }
+// Wait until all but the last committed bulk group have finished reading shared memory.
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int32_t x, int32_t y, int32_t z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
                  :: "l"(reinterpret_cast<uint64_t>(tmap)), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
@@ -729,18 +654,121 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t cluster_addr) {
     return v;
 }
 
-constexpr int kStageOut = 4096;            // an epilogue warp's outgoing 32 rows of 128 bytes
+
+// The parts of a tile's sum, ROWS rows of 128 results at pitch PITCH in the ring of each CTA of
+// the cluster: each CTA takes its share of the rows, adds the parts in rank order and finishes
+// them.  U rows per warp at a time: their loads from the other CTAs are in flight together.
+template <int ROWS, int PITCH>
+__device__ __forceinline__ void join(const Args& a, const Work& w, uint32_t ring, int warp, int lane, int tc, int tr) {
+    constexpr int U = ROWS >= 64 ? 4 : ROWS / 16;
+    const int j0 = ROWS * (int)w.rank / a.split, j1 = ROWS * ((int)w.rank + 1) / a.split;
+    const int c = tc * 128 + lane * 4, n = min(4, a.C - c);
+    for (int j = j0 + warp; j < j1; j += kEpiWarps * U) {
+        float z[U][4];
+        #pragma unroll
+        for (int u = 0; u < U; ++u) z[u][0] = z[u][1] = z[u][2] = z[u][3] = 0.f;
+        #pragma unroll 2
+        for (int p = 0; p < a.split; ++p) {
+            const uint32_t from = map_to(ring + (uint32_t)(j * PITCH + lane * 4) * 4, p);
+            float4 x[U];
+            #pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (j + u * kEpiWarps < j1) x[u] = ld_peer4(from + u * kEpiWarps * PITCH * 4);
+            #pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (j + u * kEpiWarps < j1) {
+                    z[u][0] += x[u].x; z[u][1] += x[u].y; z[u][2] += x[u].z; z[u][3] += x[u].w;
+                }
+        }
+        #pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = (int64_t)tr * ROWS + j + u * kEpiWarps;
+            if (j + u * kEpiWarps < j1 && r < a.R && n > 0) {
+                finish<4>(a, z[u], r, c, n);
+                store_row<4>(a, z[u], r, c, n);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- few rows
+// Lanes are columns c of C, accumulator columns its rows.  Grid: a cluster of `split` CTAs per
+// tile of 128 c; the parts of the sum meet in shared memory and are added in rank order.
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 2)
+k_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a) {
+    using F = Cfg<1, BN>;
+    constexpr int ST = F::kStages, H = F::kHalf, E = H < 16 ? H : 16;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Bars<ST> sm;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const Work w = work_of<1>(a);
+    const uint32_t tmem = start<1, BN, ST>(sm, warp);
+    int tc, tr;
+    tile_at(a, w.first, tc, tr);
+    if (warp == kEpiWarps) {
+        produce<1, BN, false, ST>(&tm_a, &tm_b, a, w, sm, ring);
+    } else if (warp == kEpiWarps + 1) {
+        issue<1, BN, ST>(a, w, sm, ring, tmem);
+    } else {
+        const int q = warp & 3, half = warp >> 2;
+        const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + half * H;
+        float v[H];
+        bool ok = true;
+        for (int ch = 0; ch < w.nch; ++ch) {
+            const int buf = ch & 1;
+            if (!warp_wait(&sm.acc_full[buf], (ch / 2) & 1, a.err, 3301)) { ok = false; break; }
+            tc_fence_after();
+            add_columns<H>(at0 + buf * BN, v, ch == 0);
+            release<1>(sm, buf, lane);
+        }
+        if (!ok) {
+            // the status block says so; the results are not complete
+        } else if (a.split > 1) {
+            // column j of the tile at part[j][c].  The stages' memory is free: this tile is the
+            // block's only one and its last product is done.
+            float* part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));
+            #pragma unroll
+            for (int e = 0; e < H; ++e) part[(half * H + e) * 128 + q * 32 + lane] = v[e];
+        } else {
+            const Lane l = lane_of(a, tc * 128 + q * 32 + lane);
+            const int64_t r0 = (int64_t)tr * BN + half * H;
+            #pragma unroll
+            for (int e = 0; e < H; e += E) {
+                const int64_t left = a.R - (r0 + e);
+                if (left > 0) emit<E>(a, l, r0 + e, left < E ? (int)left : E, v + e);
+            }
+        }
+    }
+    if (a.split > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp < kEpiWarps) join<BN, 128>(a, w, ring, warp, lane, tc, tr);
+        __syncwarp();
+        cluster_sync();                    // no CTA's memory goes while another reads it
+    }
+    finish_cta<1, BN>(tmem, warp);
+}
+
+constexpr int kStageOut = 4096;            // outgoing: 32 rows of 128 bytes, two of them per epilogue warp
+// bf16 columns of an outgoing piece: a warp's BN / 2 columns in rows of 128 bytes, or of 64 where
+// they are no multiple of that.  (fp32 pieces are 32 columns, 128 bytes.)
+template <int BN>
+__host__ __device__ constexpr int out_piece() { return BN % 128 == 0 ? 64 : 32; }
+// Chunk c (of 4) of row r in 64-byte rows swizzled by TMA's 64-byte mode.
+__device__ __forceinline__ uint32_t swz64(int r, int c) { return (uint32_t)r * 64u + (uint32_t)((c ^ ((r >> 1) & 3)) << 4); }
 template <int CG, int BN>
-constexpr int tile_smem() { return Cfg<CG, BN>::kRing + (CG == 2 ? kEpiWarps * kStageOut : 0) + 1024; }
+constexpr int tile_smem() { return Cfg<CG, BN>::kRing + (CG == 2 ? 2 * kEpiWarps * kStageOut : 0) + 1024; }
 constexpr int kPartPitch = 132;            // floats per row of a part (CG 1): rows start 4 banks apart
 
 // Lanes are rows of C.  Grid: pairs (CG 2) walk the tiles; or a cluster of `split` CTAs per tile.
 template <int CG, int BN>
-__global__ void __launch_bounds__(kThreads, CG == 2 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, 1)
 k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
        const __grid_constant__ CUtensorMap tm_y, const Args a) {
     using F = Cfg<CG, BN>;
-    constexpr int ST = F::kStages, H = F::kHalf;
+    constexpr int ST = F::kStages, H = F::kHalf, P = out_piece<BN>();
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<ST> sm;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -754,7 +782,8 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
     } else {
         const int q = warp & 3, half = warp >> 2;
         const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + half * H;
-        const uint32_t stage = ring + F::kRing + warp * kStageOut;
+        const uint32_t stages = ring + F::kRing + warp * 2 * kStageOut;
+        uint32_t flip = 0;
         const bool parts = CG == 1 && a.split > 1;
         int ac = 0;
         bool ok = true;
@@ -800,17 +829,22 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                 uint32_t u[32];
                 PRISM_TMEM_LD32(at0 + buf * BN + e, u);
                 tmem_wait_ld();
+                // the accumulator is free once its last columns are in registers
+                if (e + 32 >= H || c + 32 >= a.C) release<CG>(sm, buf, lane);
                 float z[32];
                 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
                 finish<32>(a, z, r0 + lane, c, n);
                 if (CG == 2 && a.y_tma) {
-                    // 32 columns are a whole 128-byte row of the stage in fp32, half of one in bf16
-                    const bool begin = a.y.f32 || !(e & 32), end = a.y.f32 || (e & 32) || e + 32 >= H || c + 32 >= a.C;
+                    // 32 columns are a whole row of the stage, or half of one of 64 bf16
+                    const bool wide = P == 64 && !a.y.f32;
+                    const bool begin = !wide || !(e & 32), end = !wide || (e & 32) || c + 32 >= a.C;
                     if (begin) {
-                        if (lane == 0) bulk_wait_read0();      // the stage's last store has read it
+                        flip ^= kStageOut;                     // the other stage,
+                        if (lane == 0) bulk_wait_read1();      // once its last store has read it
                         __syncwarp();
                     }
+                    const uint32_t stage = stages + flip;
                     if (a.y.f32) {
                         #pragma unroll
                         for (int k = 0; k < 8; ++k)
@@ -819,16 +853,16 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                     } else {
                         #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            st_shared_v4(stage + swz128(lane, (e & 32) / 8 + k), pack_bf16(z[8 * k], z[8 * k + 1]),
-                                         pack_bf16(z[8 * k + 2], z[8 * k + 3]), pack_bf16(z[8 * k + 4], z[8 * k + 5]),
-                                         pack_bf16(z[8 * k + 6], z[8 * k + 7]));
+                            st_shared_v4(stage + (P == 64 ? swz128(lane, (e & 32) / 8 + k) : swz64(lane, k)),
+                                         pack_bf16(z[8 * k], z[8 * k + 1]), pack_bf16(z[8 * k + 2], z[8 * k + 3]),
+                                         pack_bf16(z[8 * k + 4], z[8 * k + 5]), pack_bf16(z[8 * k + 6], z[8 * k + 7]));
                     }
                     if (end) {
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
                             // what lies outside C is not written
-                            const int cs = a.y.f32 ? c : c & ~63;
+                            const int cs = wide ? c & ~63 : c;
                             const int zh = a.y.hd ? cs / a.y.hd : 0;
                             tma_store_3d(&tm_y, stage, cs - zh * a.y.hd, (int)r0, zh);
                             bulk_commit();
@@ -839,31 +873,17 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                 }
                 __syncwarp();
             }
-            release<CG>(sm, buf, lane);
+            if (c0 >= a.C) release<CG>(sm, buf, lane);         // (a tile's half without columns)
         }
         if (CG == 2 && lane == 0) bulk_wait0();
     }
     if (CG == 1 && a.split > 1) {
         __syncwarp();
         cluster_sync();
-        // each CTA of the cluster finishes its share of the rows, the parts added in rank order
         if (warp < kEpiWarps) {
             int tc, tr;
             tile_at(a, w.first, tc, tr);
-            const int j0 = 128 * (int)w.rank / a.split, j1 = 128 * ((int)w.rank + 1) / a.split;
-            const int c = tc * BN + lane * 4, n = min(4, a.C - c);
-            for (int j = j0 + warp; j < j1; j += kEpiWarps) {
-                const int64_t r = (int64_t)tr * 128 + j;
-                if (r >= a.R || n <= 0) continue;
-                const uint32_t my = ring + (uint32_t)(j * kPartPitch + lane * 4) * 4;
-                float z[4] = {0.f, 0.f, 0.f, 0.f};
-                for (int p = 0; p < a.split; ++p) {
-                    const float4 x = ld_peer4(map_to(my, p));
-                    z[0] += x.x; z[1] += x.y; z[2] += x.z; z[3] += x.w;
-                }
-                finish<4>(a, z, r, c, n);
-                store_row<4>(a, z, r, c, n);
-            }
+            join<128, kPartPitch>(a, w, ring, warp, lane, tc, tr);
         }
         __syncwarp();
         cluster_sync();                    // no CTA's memory goes while another reads it
@@ -1031,17 +1051,19 @@ static int make_operand(CUtensorMap* m, Operand* o, const Matrix& x, bool mn, in
     return r == CUDA_SUCCESS ? PRISM_OK : PRISM_ERR_CUDA;
 }
 
-// C as boxes of 32 rows by 128 bytes.
-static int make_out_map(CUtensorMap* m, const Out& y, int64_t R, int C) {
+// C as boxes of 32 rows by 128 bytes (64 bytes: bf16 pieces of 32 columns).
+static int make_out_map(CUtensorMap* m, const Out& y, int64_t R, int C, int piece) {
     auto enc = encode_fn();
     if (!enc) return PRISM_ERR_CUDA;
     const int e = y.f32 ? 4 : 2;
     cuuint64_t dims[3] = {(cuuint64_t)(y.hd ? y.hd : C), (cuuint64_t)R, (cuuint64_t)(y.hd ? C / y.hd : 1)};
     cuuint64_t strides[2] = {(cuuint64_t)y.rs * e, (cuuint64_t)(y.hd ? y.hs : R * y.rs) * e};
-    cuuint32_t boxd[3] = {(cuuint32_t)(128 / e), 32, 1};
+    const bool half = !y.f32 && piece == 32;
+    cuuint32_t boxd[3] = {(cuuint32_t)(y.f32 ? 32 : piece), 32, 1};
     cuuint32_t es[3] = {1, 1, 1};
     CUresult r = enc(m, y.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, y.p, dims, strides,
-                     boxd, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                     boxd, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PRISM_OK : PRISM_ERR_CUDA;
 }
@@ -1054,7 +1076,15 @@ struct Shape {
 };
 
 // The tile of a product of R rows, C columns and kb stages.
-static Shape shape_of(int64_t R, int64_t C, int kb, bool x_mn) {
+//   up to 64 rows: k_few, its contraction split until two CTAs run on every SM.
+//   else the least of the estimates, in cycles of one SM:
+//     pairs on 256 x bn tiles: their waves over 74 pairs, each kb stages of 2.03 bn cycles (measured:
+//       518 at 256; the instruction's own 512) and 2,500 to fill and drain; 8,000 to start;
+//     single CTAs on 128 x 128 tiles, `split` to a tile: all at once, kb / split stages of 300 cycles,
+//       10,000 to start and 4,000 to join the parts.
+//   A tile width that fits the waves counts most: 512 rows of 5,120 by 5,120 are 80 tiles at bn = 128
+//   (two waves, 31.8 us), 40 at 256 (half of the pairs idle, 30.6 us), 54 at 192.
+static Shape shape_of(int64_t R, int64_t C, int kb, bool x_mn, bool y_mn) {
     if (R <= 64) {
         Shape s{1, 1, 64, 1};
         if (!x_mn) s.bn = R <= 16 ? 16 : R <= 32 ? 32 : 64;      // an MN-major slab has 64 rows
@@ -1062,11 +1092,21 @@ static Shape shape_of(int64_t R, int64_t C, int kb, bool x_mn) {
         while (s.split < 8 && tiles * s.split * 2 <= 2 * 148 && kb >= 8 * s.split) s.split *= 2;
         return s;
     }
-    if (ceil_div(R, 256) * ceil_div(C, 256) >= 74) return Shape{0, 2, 256, 1};
-    Shape s{0, 1, 128, 1};
+    Shape best{0, 2, 256, 1};
+    int64_t least = INT64_MAX;
+    for (int bn : {256, 192, 128}) {
+        if (bn == 192 && y_mn) continue;                         // a CTA's half is no whole slabs
+        const int64_t waves = ceil_div(ceil_div(R, 256) * ceil_div(C, bn), 74);
+        const int64_t t = 8000 + waves * ((int64_t)kb * bn * 65 / 32 + 2500);
+        if (t < least) { least = t; best = Shape{0, 2, bn, 1}; }
+    }
     const int64_t tiles = ceil_div(R, 128) * ceil_div(C, 128);
-    while (s.split < 8 && tiles * s.split * 2 <= 2 * 148 && kb >= 8 * s.split) s.split *= 2;
-    return s;
+    for (int split : {1, 2, 4, 8}) {
+        if (tiles * split > 148 || (split > 1 && kb < 4 * split)) break;
+        const int64_t t = 10000 + ceil_div(kb, split) * 300 + (split > 1 ? 4000 : 0);
+        if (t < least) { least = t; best = Shape{0, 1, 128, split}; }
+    }
+    return best;
 }
 
 // Starts `kernel` as clusters of `group` CTAs.  The shared-memory opt-in is made for every call:
@@ -1106,7 +1146,7 @@ static int product(const Matrix& X, bool x_mn, const Matrix& Y, bool y_mn, int64
     a.R = R;
     a.C = C;
     a.kblocks = (int)ceil_div(K, kKB);
-    const Shape sh = shape_of(R, C, a.kblocks, x_mn);
+    const Shape sh = shape_of(R, C, a.kblocks, x_mn, y_mn);
     a.split = sh.split;
     a.chunk = a.y.f32 ? kChunkF32 : kChunkBF16;
     a.band = 8;
@@ -1127,9 +1167,12 @@ static int product(const Matrix& X, bool x_mn, const Matrix& Y, bool y_mn, int64
     // a map of C wants its address and row stride in whole 16 bytes
     CUtensorMap to{};
     a.y_tma = sh.cg == 2 && a.y.vec;
-    if (a.y_tma) st = make_out_map(&to, a.y, R, C);
+    if (a.y_tma) st = make_out_map(&to, a.y, R, C, sh.bn % 128 == 0 ? 64 : 32);
     if (st) return st;
-    return sh.cg == 2 ? launch_tile<2, 256>(tx, ty, to, a, s) : launch_tile<1, 128>(tx, ty, to, a, s);
+    if (sh.cg == 1) return launch_tile<1, 128>(tx, ty, to, a, s);
+    return sh.bn == 256   ? launch_tile<2, 256>(tx, ty, to, a, s)
+           : sh.bn == 192 ? launch_tile<2, 192>(tx, ty, to, a, s)
+                          : launch_tile<2, 128>(tx, ty, to, a, s);
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

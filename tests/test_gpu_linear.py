@@ -52,6 +52,11 @@ SHAPES = {
     "pairs_heads": (2571, 640, 1920, 10, 15, 0, 0, 0),
     "pairs_odd": (2571, 203, 2121, 0, 0, 0, 0, 0),
     "pairs_chunks": (2500, 5000, 2000, 0, 0, 0, 0, 0),
+    "tiles_192": (520, 640, 4160, 0, 0, 0, 0, 0),
+    "tiles_192_ragged_heads": (500, 320, 5120, 5, 40, 0, 0, 0),
+    "tiles_128": (300, 256, 6400, 0, 0, 0, 0, 0),
+    "single_split8": (300, 8192, 300, 0, 0, 0, 0, 0),
+    "single_no_split": (70, 72, 260, 0, 0, 0, 0, 0),
     "pairs_one_column_tile": (20000, 64, 130, 0, 0, 0, 0, 0),
 }
 
