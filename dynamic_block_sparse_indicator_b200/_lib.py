@@ -544,23 +544,30 @@ def _code(dtype, what):
 
 
 class _Launch:
-    """The device and stream of a call.  Makes the tensors' device current, and, where the
-    call runs on another stream than torch's current one, tells the caching allocator that
-    the tensors are in use there (their memory is not handed out again before it is done)."""
+    """The device and stream of a call.  Makes the tensors' device current.  Where the call runs
+    on another stream than torch's current one, what it allocates comes from that stream (memory
+    that the current stream may still be using is not written) and counts as used by both, and
+    the tensors given count as used there: none is handed out again before that work is done.
+    Ordering the two streams is the caller's, as everywhere."""
 
     def __init__(self, tensors, stream):
         import torch
-        self.tensors = [t for t in tensors if t is not None]
-        dev = self.tensors[0].device
-        if any(not t.is_cuda or t.device != dev for t in self.tensors):
-            raise ValueError("the tensors must be on one CUDA device")
+        first = tensors[0]
+        dev = first.device
+        for t in tensors:
+            if t is not None and (t.device != dev or not t.is_cuda):
+                raise ValueError("the tensors must be on one CUDA device")
+        self.first, self.tensors = first, tensors
         self.guard = torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else None
-        cur = torch.cuda.current_stream(dev)
-        self.s = cur if stream is None else stream
-        if self.s.device != dev:
-            raise ValueError(f"the stream is on {self.s.device}, the tensors are on {dev}")
-        self.other = self.s.cuda_stream != cur.cuda_stream
-        self.stream = C.c_void_p(self.s.cuda_stream)
+        cur = self.cur = torch.cuda.current_stream(dev)
+        self.other = False
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+            self.other = stream.cuda_stream != cur.cuda_stream
+            cur = stream
+        self.s = cur
+        self.stream = cur.cuda_stream
 
     def __enter__(self):
         if self.guard is not None:
@@ -573,17 +580,22 @@ class _Launch:
         return False
 
     def empty(self, shape, dtype):
-        """Memory for the call (from torch's current stream, as every torch.empty)."""
+        """Memory for the call."""
+        if not self.other:
+            return self.first.new_empty(shape, dtype=dtype)
         import torch
-        t = torch.empty(shape, dtype=dtype, device=self.tensors[0].device)
-        self.tensors.append(t)
+        with torch.cuda.stream(self.s):
+            t = self.first.new_empty(shape, dtype=dtype)
+        t.record_stream(self.cur)
         return t
 
     def zero_status(self):
         """A device status block for the call, cleared on its stream."""
         import torch
         with torch.cuda.stream(self.s):
-            t = torch.zeros(4, dtype=torch.int32, device=self.tensors[0].device)
+            t = self.first.new_zeros(4, dtype=torch.int32)
+        if self.other:
+            t.record_stream(self.cur)
         return t
 
     def check(self, status, what):
@@ -591,7 +603,13 @@ class _Launch:
             raise PrismError(status, what)
         if self.other:
             for t in self.tensors:
-                t.record_stream(self.s)
+                if t is not None:
+                    t.record_stream(self.s)
+
+
+def _at(t):
+    """A tensor's address, or None."""
+    return None if t is None else t.data_ptr()
 
 
 class Rope:
@@ -599,6 +617,9 @@ class Rope:
 
     def __init__(self, table, T, H, W, dims, pairing):
         self.table, self.T, self.H, self.W, self.dims, self.pairing = table, T, H, W, tuple(dims), pairing
+
+    def __repr__(self):
+        return f"Rope({self.T} x {self.H} x {self.W}, channels {self.dims}, pairing {self.pairing})"
 
 
 def _norm_rope_params(N, heads, D, dtype, out_dtype, w_dtype, rope, eps):
@@ -620,15 +641,19 @@ def make_rope(T, H, W, dims, theta=10000.0, pairing=PRISM_PAIR_ADJACENT, first_f
     D = 64 if sum(dims) <= 64 else 128
     p = _norm_rope_params(T * H * W, 1, D, PRISM_BF16, PRISM_BF16, PRISM_F32, rope, 1.0)
     with _Launch([table], stream) as go:
-        go.check(load().prism_rope_table(C.byref(p), float(theta), int(first_frame), _ptr(table), go.stream),
+        go.check(load().prism_rope_table(C.byref(p), float(theta), int(first_frame), table.data_ptr(), go.stream),
                  "prism_rope_table")
     return rope
 
 
 def _rows(t, what):
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    """A pointer to the rows of [heads, N, D], or None."""
+    if t is None:
+        return None
+    hs, ts, cs = t.stride()
+    if cs != 1 and t.shape[2] > 1:
         raise ValueError(f"{what} must be [heads, N, D] with consecutive channels (any head and token strides)")
-    return PrismRows(t.data_ptr(), t.stride(0), t.stride(1))
+    return C.byref(PrismRows(t.data_ptr(), hs, ts))
 
 
 def _weights(ws, D, what):
@@ -641,14 +666,14 @@ def _weights(ws, D, what):
 
 def _qk_pair(named, rope):
     """Checks a list of (name, query side, key side); returns heads, N, D."""
-    shape = tuple(named[0][1].shape)
+    shape = named[0][1].shape
     if len(shape) != 3:
         raise ValueError("q must be [heads, N, D]")
+    alone = named[0][2] is None
     for name, a, b in named:
-        for t in (a, b):
-            if t is not None and tuple(t.shape) != shape:
-                raise ValueError(f"{name}: expected [heads, N, D] = {shape}, got {tuple(t.shape)}")
-        if (b is None) != (named[0][2] is None):
+        if a.shape != shape or (b is not None and b.shape != shape):
+            raise ValueError(f"{name}: expected [heads, N, D] = {tuple(shape)}")
+        if (b is None) != alone:
             raise ValueError("the key's tensors must all be given or none")
         if b is not None and b.dtype != a.dtype:
             raise ValueError(f"{name}: query and key must be of one type")
@@ -683,11 +708,9 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, rope=None, eps=1e-6, q_out=None, k
             q_out = go.empty(q.shape, out_dtype)
             k_out = go.empty(k.shape, out_dtype) if k is not None else None
         p = _norm_rope_params(N, heads, D, dt, odt, wdt, rope, eps)
-        kr = None if k is None else C.byref(_rows(k, "k"))
-        kor = None if k is None else C.byref(_rows(k_out, "k_out"))
-        go.check(load().prism_qk_norm_rope(C.byref(p), C.byref(_rows(q, "q")), kr, _ptr(wq), _ptr(wk),
-                                           _ptr(rope.table) if rope is not None else None,
-                                           C.byref(_rows(q_out, "q_out")), kor, go.stream), "prism_qk_norm_rope")
+        go.check(load().prism_qk_norm_rope(C.byref(p), _rows(q, "q"), _rows(k, "k"), _at(wq), _at(wk),
+                                           _at(rope.table) if rope is not None else None, _rows(q_out, "q_out"),
+                                           _rows(k_out, "k_out"), go.stream), "prism_qk_norm_rope")
     return q_out, k_out
 
 
@@ -727,12 +750,10 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k=None, wq=None, wk=None, rope=None, eps
         lib = load()
         if workspace is None and (dwq is not None or dwk is not None):
             workspace = go.empty((max(int(lib.prism_qk_norm_rope_bwd_workspace_bytes(C.byref(p))), 16),), torch.uint8)
-        one = lambda t, what: None if t is None else C.byref(_rows(t, what))
-        go.check(lib.prism_qk_norm_rope_bwd(C.byref(p), one(dq_out, "dq_out"), one(dk_out, "dk_out"), one(q, "q"),
-                                            one(k, "k"), _ptr(wq), _ptr(wk),
-                                            _ptr(rope.table) if rope is not None else None, one(dq, "dq"),
-                                            one(dk, "dk"), _ptr(dwq), _ptr(dwk), _ptr(workspace),
-                                            workspace.numel() * workspace.element_size() if workspace is not None else 0,
+        go.check(lib.prism_qk_norm_rope_bwd(C.byref(p), _rows(dq_out, "dq_out"), _rows(dk_out, "dk_out"), _rows(q, "q"),
+                                            _rows(k, "k"), _at(wq), _at(wk),
+                                            _at(rope.table) if rope is not None else None, _rows(dq, "dq"),
+                                            _rows(dk, "dk"), _at(dwq), _at(dwk), _at(workspace), _size(workspace),
                                             go.stream), "prism_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
@@ -805,8 +826,8 @@ def linear(x, W, bias=None, residual=None, activation=PRISM_ACT_NONE, y=None, ou
         if workspace is None and (xs % 8 or ws_ % 8):
             workspace = go.empty((max(int(lib.prism_linear_workspace_bytes(C.byref(p))), 16),), torch.uint8)
         status = go.zero_status() if status is None else status
-        go.check(lib.prism_linear(C.byref(p), _ptr(x), _ptr(W), _ptr(bias), _ptr(residual), _ptr(y), _ptr(pre),
-                                  _ptr(workspace), _size(workspace), _ptr(status), go.stream), "prism_linear")
+        go.check(lib.prism_linear(C.byref(p), x.data_ptr(), W.data_ptr(), _at(bias), _at(residual), y.data_ptr(), _at(pre),
+                                  _at(workspace), _size(workspace), status.data_ptr(), go.stream), "prism_linear")
     return y, pre, status
 
 
@@ -838,12 +859,12 @@ def linear_bwd(dy, x, W, pre=None, activation=PRISM_ACT_NONE, dx=None, dW=None, 
                           _code(dw_dtype, "dW"), xs, ws_, ys, N)
     lib = load()
     with _Launch([dy, x, W, pre, dx, dW, db, workspace, status], stream) as go:
-        dx = go.empty(tuple(x.shape), torch.bfloat16) if dx is None and want_dx else dx
+        dx = go.empty(x.shape, torch.bfloat16) if dx is None and want_dx else dx
         dW = go.empty((N, K), dw_dtype) if dW is None and want_dw else dW
         db = go.empty((N,), torch.float32) if db is None and want_db else db
         if workspace is None:
             workspace = go.empty((max(int(lib.prism_linear_bwd_workspace_bytes(C.byref(p))), 16),), torch.uint8)
         status = go.zero_status() if status is None else status
-        go.check(lib.prism_linear_bwd(C.byref(p), _ptr(dy), _ptr(x), _ptr(W), _ptr(pre), _ptr(dx), _ptr(dW), _ptr(db),
-                                      _ptr(workspace), _size(workspace), _ptr(status), go.stream), "prism_linear_bwd")
+        go.check(lib.prism_linear_bwd(C.byref(p), dy.data_ptr(), x.data_ptr(), W.data_ptr(), _at(pre), _at(dx), _at(dW), _at(db),
+                                      _at(workspace), _size(workspace), status.data_ptr(), go.stream), "prism_linear_bwd")
     return dx, dW, db, status
