@@ -87,12 +87,40 @@ template <> struct Vec8<float> {
     }
 };
 
-// Sum over the LANES lanes that hold one row.
-template <int LANES>
-__device__ __forceinline__ float row_sum(float v) {
+// Sums of U rows' values over the LANES lanes that hold a row: s[i] is this lane's part of row
+// i.  Each exchange halves the rows a lane still carries, so U rows cost U - 1 + log2(LANES / U)
+// shuffles instead of U log2(LANES); what follows from a row's sum is computed by the lanes that
+// own the row, owned_row() of them, and handed to all by from_owner().
+template <int U> __device__ __forceinline__ int owned_row(int lane) { return lane & (U - 1); }
+template <int LANES, int U>
+__device__ __forceinline__ float owned_sum(const float* s, int lane) {
+    static_assert(U == 1 || U == 2 || U == 4, "rows of a group");
+    float k;
+    int o = 1;
+    if (U == 4) {
+        const bool hi = lane & 1, hi2 = lane & 2;
+        float k0 = hi ? s[1 % U] : s[0], k1 = hi ? s[3 % U] : s[2 % U];
+        k0 += __shfl_xor_sync(0xffffffffu, hi ? s[0] : s[1 % U], 1);
+        k1 += __shfl_xor_sync(0xffffffffu, hi ? s[2 % U] : s[3 % U], 1);
+        k = hi2 ? k1 : k0;
+        k += __shfl_xor_sync(0xffffffffu, hi2 ? k0 : k1, 2);
+        o = 4;
+    } else if (U == 2) {
+        const bool hi = lane & 1;
+        k = hi ? s[1 % U] : s[0];
+        k += __shfl_xor_sync(0xffffffffu, hi ? s[0] : s[1 % U], 1);
+        o = 2;
+    } else {
+        k = s[0];
+    }
     #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int i = 0; i < 4; ++i, o <<= 1)
+        if (o < LANES) k += __shfl_xor_sync(0xffffffffu, k, o);
+    return k;
+}
+template <int U>
+__device__ __forceinline__ float from_owner(float v, int lane, int i) {
+    return __shfl_sync(0xffffffffu, v, (lane & ~(U - 1)) | i);
 }
 
 __device__ __forceinline__ float weight_at(const void* w, int f32, int ch) {
@@ -174,8 +202,48 @@ template <> struct Turn<true> {
     template <int DIR>
     __device__ __forceinline__ void take(float* u, const float* row) const {
         #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = u[i] * c[i] + DIR * s[i] * row[at[i]];
+        for (int i = 0; i < 8; i += 2) {
+            float p0, p1;
+            fmul2(p0, p1, row[at[i]], row[at[i + 1]], DIR * s[i], DIR * s[i + 1]);
+            ffma2(u[i], u[i + 1], u[i], u[i + 1], c[i], c[i + 1], p0, p1);
+        }
     }
+};
+
+// The rotation with a tensor's weights in it, x -> R (w x) (`w` laid out by Turn<true>::place).
+template <bool HALVES> struct Fold;
+template <> struct Fold<false> {
+    float a0[4], b0[4], a1[4], b1[4];        // y_a = x_a a0 + x_b b0, y_b = x_a a1 + x_b b1
+    __device__ __forceinline__ void init(const Rope& r, const float* w, int ch, int t, int h, int g) {
+        const float* own = w + Turn<true>::place(ch);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 cs = r.tab ? rope_at(r, (ch >> 1) + i, t, h, g) : make_float2(1.f, 0.f);
+            a0[i] = own[2 * i] * cs.x; b0[i] = -own[2 * i + 1] * cs.y;
+            a1[i] = own[2 * i] * cs.y; b1[i] = own[2 * i + 1] * cs.x;
+        }
+    }
+    __device__ __forceinline__ void apply(float* x, const float*) const {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            float p0, p1;
+            fmul2(p0, p1, b, a, b0[i], a1[i]);
+            ffma2(x[2 * i], x[2 * i + 1], a, b, a0[i], b1[i], p0, p1);
+        }
+    }
+};
+template <> struct Fold<true> {
+    Turn<true> turn;
+    __device__ __forceinline__ void init(const Rope& r, const float* w, int ch, int t, int h, int g) {
+        turn.init(r, ch, t, h, g);
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            turn.c[e] *= w[Turn<true>::place(ch) + e];
+            turn.s[e] *= w[turn.at[e]];
+        }
+    }
+    __device__ __forceinline__ void apply(float* x, const float* row) const { turn.take<1>(x, row); }
 };
 
 // Rows of a group, and shared memory for their exchange (HALVES only).
@@ -194,74 +262,79 @@ __device__ __forceinline__ void grid_at(const Rope& r, int64_t n, int& t, int& h
     w = (int)(q - (uint32_t)h * (uint32_t)r.W);
 }
 
-// Grid: x = token tiles (strided), y = head groups.  A block takes its tokens' rows of both
-// tensors, U heads at a time: U loads in flight per lane, one exchange for the group.
+// Sum of squares of a lane's eight channels, and eight products by one factor (two at a time).
+__device__ __forceinline__ float squares(const float* x) {
+    float a0, a1;
+    fmul2(a0, a1, x[0], x[1], x[0], x[1]);
+    #pragma unroll
+    for (int e = 2; e < 8; e += 2) ffma2(a0, a1, x[e], x[e + 1], x[e], x[e + 1], a0, a1);
+    return a0 + a1;
+}
+__device__ __forceinline__ void scale8(float* x, float r) {
+    #pragma unroll
+    for (int e = 0; e < 8; e += 2) fmul2(x[e], x[e + 1], x[e], x[e + 1], r, r);
+}
+
+// The forward.  Grid: x = token tiles (strided), y = head groups.  A block takes its tokens'
+// rows of both tensors, U heads at a time: U loads in flight per lane.
+// The weights are folded into the rotation, y_a = r (x_a w_a c - x_b w_b s): the factors are made
+// once per token and tensor, and with halves the rows pass through shared memory as they were
+// read, so a group's exchange does not wait for its norms.  At 40 heads of 92,160 tokens adjacent
+// pairs move 6.3 TB/s (64 registers for 4 blocks per SM; 3 blocks 6.2, 6 blocks with U = 2 5.5) and
+// halves 5.3: there shared memory is 82% busy, eight words written and eight read per lane and row
+// (unfolded, every row summed by itself: 4.3).  At 5 heads, 1,013,760 tokens, 5.1: a token's factors
+// and addresses serve ten rows only.
 template <typename TI, typename TO, int D, bool HALVES>
 __global__ void __launch_bounds__(kThreads, HALVES ? 3 : 4) k_norm_rope(const Args a) {
     constexpr int U = sizeof(TI) == 2 ? 4 : 2;
     using G = Group<TI, D, HALVES, U>;
     constexpr int LANES = D / 8, RPB = G::kRows;
     __shared__ float sx[G::kFloats];
-    __shared__ float4 sw[2][D / 4];
-    const int ch = (threadIdx.x % LANES) * 8, sub = threadIdx.x / LANES;
+    __shared__ float sw[2][D + D / 8];
+    const int lane = threadIdx.x & 31, ch = (threadIdx.x % LANES) * 8, sub = threadIdx.x / LANES;
     float* row = HALVES ? sx + sub * G::kPitch : sx;
     const int h0 = blockIdx.y * a.hpc, h1 = min(h0 + a.hpc, a.heads);
     for (int i = threadIdx.x; i < a.tensors * D; i += kThreads)
-        reinterpret_cast<float*>(sw)[i] = weight_at(a.w[i / D], a.w_f32, i % D);
+        sw[i / D][Turn<true>::place(i % D)] = weight_at(a.w[i / D], a.w_f32, i % D);
     __syncthreads();
     for (int64_t n0 = (int64_t)blockIdx.x * RPB; n0 < a.N; n0 += (int64_t)gridDim.x * RPB) {
         const int64_t n = n0 + sub;
         const bool ok = n < a.N;
-        Turn<HALVES> turn;
-        if (a.rope.tab) {
-            int t, h, w;
-            grid_at(a.rope, ok ? n : 0, t, h, w);
-            turn.init(a.rope, ch, t, h, w);
-        }
+        int gt = 0, gh = 0, gw = 0;
+        if (a.rope.tab) grid_at(a.rope, ok ? n : 0, gt, gh, gw);
         for (int z = 0; z < a.tensors; ++z) {
-            const TI* src = static_cast<const TI*>(a.in[z].p) + n * a.in[z].ts + ch;
-            TO* dst = static_cast<TO*>(a.out[z].p) + n * a.out[z].ts + ch;
-            for (int h = h0; h < h1; h += U) {
+            Fold<HALVES> fold;
+            fold.init(a.rope, sw[z], ch, gt, gh, gw);
+            const TI* src = static_cast<const TI*>(a.in[z].p) + n * a.in[z].ts + h0 * a.in[z].hs + ch;
+            TO* dst = static_cast<TO*>(a.out[z].p) + n * a.out[z].ts + h0 * a.out[z].hs + ch;
+            for (int h = h0; h < h1; h += U, src += U * a.in[z].hs, dst += U * a.out[z].hs) {
                 Vec8<TI> v[U];
                 float r[U];
                 #pragma unroll
                 for (int i = 0; i < U; ++i) {
                     v[i] = Vec8<TI>{};
-                    if (ok && h + i < h1) v[i].load(src + (h + i) * a.in[z].hs);
+                    if (ok && h + i < h1) v[i].load(src + i * a.in[z].hs);
                 }
+                if (HALVES) __syncwarp();            // the previous group's reads are done
                 #pragma unroll
                 for (int i = 0; i < U; ++i) {
                     float x[8];
                     v[i].get(x);
-                    r[i] = x[0] * x[0];
-                    #pragma unroll
-                    for (int e = 1; e < 8; ++e) r[i] = fmaf(x[e], x[e], r[i]);
+                    if (HALVES) Turn<true>::put(x, row + i * RPB * G::kPitch, ch);
+                    r[i] = squares(x);
                 }
+                if (HALVES) __syncwarp();
+                const float own = rsqrtf(owned_sum<LANES, U>(r, lane) * (1.f / D) + a.eps);
                 #pragma unroll
-                for (int i = 0; i < U; ++i) r[i] = rsqrtf(row_sum<LANES>(r[i]) * (1.f / D) + a.eps);
-                float w[8];
-                read_w(sw[z], ch, w);
-                if (HALVES && a.rope.tab) {
-                    __syncwarp();                    // the previous group's reads are done
-                    #pragma unroll
-                    for (int i = 0; i < U; ++i) {
-                        float x[8];
-                        v[i].get(x);
-                        #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = x[e] * r[i] * w[e];
-                        turn.put(x, row + i * RPB * G::kPitch, ch);
-                    }
-                    __syncwarp();
-                }
+                for (int i = 0; i < U; ++i) r[i] = from_owner<U>(own, lane, i);
                 #pragma unroll
                 for (int i = 0; i < U; ++i) {
                     if (h + i >= h1) break;          // the same for the whole block
                     float x[8];
                     v[i].get(x);
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = x[e] * r[i] * w[e];
-                    if (a.rope.tab) turn.template take<1>(x, row + i * RPB * G::kPitch);
-                    if (ok) Vec8<TO>::store(dst + (h + i) * a.out[z].hs, x);
+                    fold.apply(x, row + i * RPB * G::kPitch);
+                    scale8(x, r[i]);
+                    if (ok) Vec8<TO>::store(dst + i * a.out[z].hs, x);
                 }
             }
         }
@@ -280,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_rope_bwd(const Args a) {
     constexpr int kSum = RPB * D;
     __shared__ float sx[kSum > G::kFloats ? kSum : G::kFloats];
     __shared__ float4 sw[1][D / 4];
-    const int z = blockIdx.z, ch = (threadIdx.x % LANES) * 8, sub = threadIdx.x / LANES;
+    const int lane = threadIdx.x & 31, z = blockIdx.z, ch = (threadIdx.x % LANES) * 8, sub = threadIdx.x / LANES;
     float* row = HALVES ? sx + sub * G::kPitch : sx;
     const int h0 = blockIdx.y * a.hpc, h1 = min(h0 + a.hpc, a.heads);
     float dw[8];
@@ -322,29 +395,57 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_rope_bwd(const Args a) {
                 }
                 __syncwarp();
             }
-            float w[8];
+            // (with halves the rotated rows stay in registers: reading the exchange twice cost 13% of the
+            // bandwidth; adjacent pairs are rotated again, from fewer registers)
+            float w[8], r[U], k[U], kept[HALVES ? U : 1][8];
             read_w(sw[0], ch, w);
             #pragma unroll
             for (int i = 0; i < U; ++i) {
-                if (h + i >= h1) break;              // the same for the whole block
-                float x[8], g[8], ss = 0.f, dot = 0.f;
+                float x[8], g[8], d0 = 0.f, d1 = 0.f;
                 v[i].get(x);
                 q[i].get(g);
                 if (a.rope.tab) turn.template take<-1>(g, row + i * RPB * G::kPitch);
-                #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ss = fmaf(x[e], x[e], ss);
-                    dot = fmaf(g[e] * w[e], x[e], dot);
+                if (HALVES) {
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) kept[HALVES ? i : 0][e] = g[e];
                 }
-                ss = row_sum<LANES>(ss);
-                dot = row_sum<LANES>(dot);
-                const float r = rsqrtf(ss * (1.f / D) + a.eps);
-                const float k = dot * r * r * (1.f / D);
+                r[i] = squares(x);
                 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < 8; e += 2) {
+                    float p0, p1;
+                    fmul2(p0, p1, g[e], g[e + 1], w[e], w[e + 1]);
+                    ffma2(d0, d1, p0, p1, x[e], x[e + 1], d0, d1);
+                }
+                k[i] = d0 + d1;
+            }
+            {
+                const float ro = rsqrtf(owned_sum<LANES, U>(r, lane) * (1.f / D) + a.eps);
+                const float ko = owned_sum<LANES, U>(k, lane) * ro * ro * ro * (-1.f / D);   // -r^3 mean(w v x)
+                #pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    r[i] = from_owner<U>(ro, lane, i);
+                    k[i] = from_owner<U>(ko, lane, i);
+                }
+            }
+            #pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (h + i >= h1) break;              // the same for the whole block
+                float x[8], g[8];
+                v[i].get(x);
+                if (HALVES) {
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] = kept[HALVES ? i : 0][e];
+                } else {
+                    q[i].get(g);
+                    if (a.rope.tab) turn.template take<-1>(g, nullptr);
+                }
+                scale8(g, r[i]);                     // r v
+                #pragma unroll
+                for (int e = 0; e < 8; e += 2) {
                     // a token behind the last one has x = g = 0 and adds nothing
-                    dw[e] = fmaf(g[e], x[e] * r, dw[e]);
-                    x[e] = r * (g[e] * w[e] - k * x[e]);
+                    ffma2(dw[e], dw[e + 1], g[e], g[e + 1], x[e], x[e + 1], dw[e], dw[e + 1]);
+                    fmul2(x[e], x[e + 1], x[e], x[e + 1], k[i], k[i]);
+                    ffma2(x[e], x[e + 1], g[e], g[e + 1], w[e], w[e + 1], x[e], x[e + 1]);
                 }
                 if (ok) Vec8<TI>::store(dst + (h + i) * a.out[z].hs, x);
             }
@@ -486,18 +587,20 @@ static int device_ok() {
 struct Grid {
     int x, y, z, hpc;
 };
+constexpr int kFwdPerSM = 32, kBwdPerSM = 8;
 
 // Blocks of a call.  One block takes every head of its tokens (its cos and sin are then
 // read once) unless that leaves fewer blocks than two per SM: then the heads are split.
-// The number of token tiles in flight is capped at 8 blocks per SM, the rest are walked.
-static Grid grid_of(int64_t N, int heads, int D, int z) {
+// Token tiles beyond `per_sm` blocks per SM are walked: 8 in the backward, whose blocks each leave
+// a row of partial sums, 32 in the forward (2% faster there than 8).
+static Grid grid_of(int64_t N, int heads, int D, int z, int per_sm) {
     const int64_t rpb = kThreads / (D / 8), tiles = (N + rpb - 1) / rpb;
     Grid g;
     g.z = z;
     g.hpc = heads;
     while (g.hpc > 1 && tiles * ((heads + g.hpc - 1) / g.hpc) * z < 2 * 148) g.hpc = (g.hpc + 1) / 2;
     g.y = (heads + g.hpc - 1) / g.hpc;
-    const int64_t cap = 8 * 148 / ((int64_t)g.y * z) > 1 ? 8 * 148 / ((int64_t)g.y * z) : 1;
+    const int64_t most = (int64_t)per_sm * 148 / ((int64_t)g.y * z), cap = most > 1 ? most : 1;
     g.x = (int)(tiles < cap ? tiles : cap);
     return g;
 }
@@ -513,12 +616,17 @@ static Rope rope_of(const prism_norm_rope_params* p, const float* table) {
 template <typename TI, typename TO, bool BWD>
 static void launch(const Args& a, const Grid& g, int D, bool halves, cudaStream_t s) {
     const dim3 grid(g.x, g.y, g.z);
-#define PRISM_NR(DD, HH)                                                        \
-    (BWD ? k_norm_rope_bwd<TI, TO, DD, HH><<<grid, kThreads, 0, s>>>(a)         \
-         : k_norm_rope<TI, TO, DD, HH><<<grid, kThreads, 0, s>>>(a))
-    if (D == 128) halves ? PRISM_NR(128, true) : PRISM_NR(128, false);
-    else halves ? PRISM_NR(64, true) : PRISM_NR(64, false);
-#undef PRISM_NR
+    if constexpr (BWD) {
+        if (D == 128) halves ? k_norm_rope_bwd<TI, TO, 128, true><<<grid, kThreads, 0, s>>>(a)
+                             : k_norm_rope_bwd<TI, TO, 128, false><<<grid, kThreads, 0, s>>>(a);
+        else halves ? k_norm_rope_bwd<TI, TO, 64, true><<<grid, kThreads, 0, s>>>(a)
+                    : k_norm_rope_bwd<TI, TO, 64, false><<<grid, kThreads, 0, s>>>(a);
+    } else {
+        if (D == 128) halves ? k_norm_rope<TI, TO, 128, true><<<grid, kThreads, 0, s>>>(a)
+                             : k_norm_rope<TI, TO, 128, false><<<grid, kThreads, 0, s>>>(a);
+        else halves ? k_norm_rope<TI, TO, 64, true><<<grid, kThreads, 0, s>>>(a)
+                    : k_norm_rope<TI, TO, 64, false><<<grid, kThreads, 0, s>>>(a);
+    }
 }
 
 template <bool BWD>
@@ -537,7 +645,7 @@ static int dispatch(const prism_norm_rope_params* p, const Args& a, const Grid& 
 static Rows rows_of(const prism_rows* r) { return Rows{r->data, r->head_stride, r->token_stride}; }
 
 static int64_t part_rows(int64_t N, int heads, int D, int z) {
-    const Grid g = grid_of(N, heads, D, z);
+    const Grid g = grid_of(N, heads, D, z, kBwdPerSM);
     return (int64_t)g.x * g.y * g.z;
 }
 
@@ -601,7 +709,7 @@ extern "C" int prism_qk_norm_rope(const prism_norm_rope_params* p, const prism_r
     a.N = p->N;
     a.heads = p->heads;
     a.eps = p->eps;
-    const Grid g = grid_of(p->N, p->heads, D, 1);
+    const Grid g = grid_of(p->N, p->heads, D, 1, kFwdPerSM);
     a.hpc = g.hpc;
     nvtxRangePushA("prism qk norm rope");
     const int st = dispatch<false>(p, a, g, static_cast<cudaStream_t>(stream));
@@ -672,7 +780,7 @@ extern "C" int prism_qk_norm_rope_bwd(const prism_norm_rope_params* p, const pri
     a.N = p->N;
     a.heads = p->heads;
     a.eps = p->eps;
-    const Grid g = grid_of(p->N, p->heads, D, z);
+    const Grid g = grid_of(p->N, p->heads, D, z, kBwdPerSM);
     a.hpc = g.hpc;
     a.part = want ? static_cast<float*>(workspace) : nullptr;
     nvtxRangePushA("prism qk norm rope bwd");

@@ -4,7 +4,8 @@
 Forward, u = x r w with r = rsqrt(mean x^2 + eps): a row's sum of squares takes at most 8 fused
 adds in a lane and 4 across lanes, one product and one sum more (14 roundings, halved by the
 root), rsqrtf is within 2 ulp (4 half steps), x r w takes 2: u is within 13 half steps; the
-rotation adds 2 and the table's rounding 1: y is within 16 EPS32 (|u_a c| + |u_b s|).
+rotation adds 2 and the table's rounding 1: y is within 16 EPS32 (|u_a c| + |u_b s|).  Folded as
+r (x_a w_a c + x_b w_b s) it is the table's 1, products 2, sum 1, r's 11 and its product 1: the same 16.
 
 Gradients: v = R^T g is within 3 EPS32 (|g_a c| + |g_b s|) =: 3 EPS32 V.  dot = sum w v x over D
 channels: 12 sums, 2 products and v's 3: within 17 EPS32 sum w V |x|.  r is within 11, so
