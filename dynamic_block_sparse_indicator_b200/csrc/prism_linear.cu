@@ -21,8 +21,8 @@
 //           N of the instruction instead of an M tile of padding.  Bound by HBM's read of W;
 //           a cluster splits the contraction.
 //
-// Warp roles: 0-7 epilogue (TMEM lane quarter w % 4, column half w / 4), 8 TMA producer and
-// TMEM allocator, 9 MMA issuer.  Two TMEM accumulators alternate, so the next products run
+// Warp roles: epilogue warps (TMEM lane quarter w % 4, columns by w / 4), then a TMA producer that
+// also allocates TMEM, then the MMA issuer.  Two TMEM accumulators alternate, so the next products run
 // while the epilogue reads the last.
 //
 // The tensor core's fp32 accumulation truncates: over a contraction of 16,384 the result
@@ -44,8 +44,6 @@
 namespace prism {
 namespace lin {
 
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = (kEpiWarps + 2) * 32;
 constexpr int kKB = 64;                    // contraction elements per stage (128-byte rows)
 constexpr int kChunkF32 = 12;              // stages per accumulation chunk (see above): 768 elements
 constexpr int kChunkBF16 = 256;            // and 16,384 where the result keeps 16 bits
@@ -311,7 +309,11 @@ struct Cfg {
     // the pair's CTAs and the single one have an SM to themselves; k_few's run two per SM
     static constexpr int kStages = (CG == 2 ? 163840 : BN >= 128 ? 196608 : 98304) / kStage;
     static constexpr int kCols = BN > 128 ? 512 : BN > 64 ? 256 : BN > 32 ? 128 : BN > 16 ? 64 : 32;   // 2 BN, a power of two
-    static constexpr int kHalf = BN / 2;                     // columns per epilogue warp
+    // epilogue: a warpgroup per 64 columns of a wide tile (the sums of 64 columns fit a thread's
+    // registers beside the rest: with 128, and half the warps, they spilled), two on a narrow one
+    static constexpr int kCol = BN >= 128 ? 64 : BN / 2;     // columns per epilogue warp
+    static constexpr int kEpi = 4 * (BN / kCol);             // epilogue warps
+    static constexpr int kThreads = (kEpi + 2) * 32;
     static constexpr int kRing = kStages * kStage;
 };
 
@@ -360,11 +362,11 @@ __device__ __forceinline__ uint32_t start(Bars<ST>& sm, int warp) {
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.acc_full[i], 1);
-            mbar_init(&sm.acc_empty[i], kEpiWarps * CG);
+            mbar_init(&sm.acc_empty[i], Cfg<CG, BN>::kEpi * CG);
         }
         mbar_fence_init();
     }
-    if (warp == kEpiWarps) {
+    if (warp == Cfg<CG, BN>::kEpi) {
         __syncwarp();
         alloc_tmem<CG>(&sm.tmem_base, Cfg<CG, BN>::kCols);
     }
@@ -382,7 +384,7 @@ __device__ __forceinline__ void finish_cta(uint32_t tmem, int warp) {
     if (CG == 2) cluster_sync();           // the pair's other CTA may still signal this one's barriers
     else __syncthreads();
     tc_fence_after();
-    if (warp == kEpiWarps) {
+    if (warp == Cfg<CG, BN>::kEpi) {
         __syncwarp();
         free_tmem<CG>(tmem, Cfg<CG, BN>::kCols);
     }
@@ -507,7 +509,7 @@ __device__ __forceinline__ void issue(const Args& a, const Work& w, Bars<ST>& sm
 // An epilogue warp's columns of an accumulator added to v (or taken, from the first chunk).
 template <int H>
 __device__ __forceinline__ void add_columns(uint32_t t, float* v, bool take) {
-    constexpr int CH = H < 16 ? H : 16;
+    constexpr int CH = 8;
     #pragma unroll
     for (int i = 0; i < H / CH; ++i) {
         uint32_t u[CH];
@@ -529,7 +531,8 @@ __device__ __forceinline__ void release(Bars<ST>& sm, int buf, int lane) {
 
 // ---------------------------------------------------------------- rows of results
 // NC results of row r from column c on (bias, kept z, activation, residual), n of them inside C.
-template <int NC>
+// ACT false: bias and residual alone; RES false: no residual.
+template <int NC, bool ACT = true, bool RES = true>
 __device__ __forceinline__ void finish(const Args& a, float* z, int64_t r, int c, int n) {
     if (a.bias) {
         if (n == NC) {
@@ -554,7 +557,7 @@ __device__ __forceinline__ void finish(const Args& a, float* z, int64_t r, int c
                                               : __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[c + i]);
         }
     }
-    if (a.pre.p && r < a.R) {
+    if (ACT && a.pre.p && r < a.R) {
         // the kept z has the operands' 16 bits: the backward forms dz from it for 16-bit products
         __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.pre.p) + at(a.pre, c) + r * a.pre.rs;
         if (a.pre.vec && n == NC) {
@@ -567,7 +570,7 @@ __device__ __forceinline__ void finish(const Args& a, float* z, int64_t r, int c
                 if (i < n) p[i] = __float2bfloat16_rn(z[i]);
         }
     }
-    switch (a.act) {
+    if (ACT) switch (a.act) {
         case PRISM_ACT_GELU:
             #pragma unroll
             for (int i = 0; i < NC; ++i) z[i] = act_of(z[i], PRISM_ACT_GELU);
@@ -582,7 +585,7 @@ __device__ __forceinline__ void finish(const Args& a, float* z, int64_t r, int c
             break;
         default: break;
     }
-    if (a.res.p && r < a.R) {
+    if (RES && a.res.p && r < a.R) {
         if (a.res.f32) {
             const float* p = static_cast<const float*>(a.res.p) + at(a.res, c) + r * a.res.rs;
             if (a.res.vec && n == NC) {
@@ -617,6 +620,29 @@ __device__ __forceinline__ void finish(const Args& a, float* z, int64_t r, int c
         }
     }
 }
+// Row r's H sums from column c on before the first product: residual and bias.  The residual is
+// read straight into the sums, every load in flight at once.
+template <int H>
+__device__ __forceinline__ void first_sums(const Args& a, float* v, int64_t r, int c) {
+    #pragma unroll
+    for (int e = 0; e < H; ++e) v[e] = 0.f;
+    if (a.res.p && a.res.f32 && a.res.vec && c + H <= a.C && r < a.R) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.res.p) + at(a.res, c) + r * a.res.rs);
+        #pragma unroll
+        for (int e = 0; e < H; e += 4) {
+            const float4 x = p[e / 4];
+            v[e] = x.x; v[e + 1] = x.y; v[e + 2] = x.z; v[e + 3] = x.w;
+        }
+        #pragma unroll
+        for (int e = 0; e < H; e += 8) finish<8, false, false>(a, v + e, r, c + e, 8);
+        return;
+    }
+    #pragma unroll
+    for (int e = 0; e < H; e += 8) {
+        const int n = min(8, a.C - (c + e));
+        if (n > 0) finish<8, false>(a, v + e, r, c + e, n);
+    }
+}
 // The same results stored by the thread itself.
 template <int NC>
 __device__ __forceinline__ void store_row(const Args& a, const float* z, int64_t r, int c, int n) {
@@ -644,8 +670,6 @@ __device__ __forceinline__ void store_row(const Args& a, const float* z, int64_t
         }
     }
 }
-// Wait until all but the last committed bulk group have finished reading shared memory.
-__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int32_t x, int32_t y, int32_t z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
                  :: "l"(reinterpret_cast<uint64_t>(tmap)), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
@@ -661,12 +685,13 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t cluster_addr) {
 // The parts of a tile's sum, ROWS rows of 128 results at pitch PITCH in the ring of each CTA of
 // the cluster: each CTA takes its share of the rows, adds the parts in rank order and finishes
 // them.  U rows per warp at a time: their loads from the other CTAs are in flight together.
+constexpr int kJoinWarps = 8;              // the epilogue warps of the kernels that split
 template <int ROWS, int PITCH>
 __device__ __forceinline__ void join(const Args& a, const Work& w, uint32_t ring, int warp, int lane, int tc, int tr) {
     constexpr int U = ROWS >= 64 ? 4 : ROWS / 16;
     const int j0 = ROWS * (int)w.rank / a.split, j1 = ROWS * ((int)w.rank + 1) / a.split;
     const int c = tc * 128 + lane * 4, n = min(4, a.C - c);
-    for (int j = j0 + warp; j < j1; j += kEpiWarps * U) {
+    for (int j = j0 + warp; j < j1; j += kJoinWarps * U) {
         float z[U][4];
         #pragma unroll
         for (int u = 0; u < U; ++u) z[u][0] = z[u][1] = z[u][2] = z[u][3] = 0.f;
@@ -676,17 +701,17 @@ __device__ __forceinline__ void join(const Args& a, const Work& w, uint32_t ring
             float4 x[U];
             #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (j + u * kEpiWarps < j1) x[u] = ld_peer4(from + u * kEpiWarps * PITCH * 4);
+                if (j + u * kJoinWarps < j1) x[u] = ld_peer4(from + u * kJoinWarps * PITCH * 4);
             #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (j + u * kEpiWarps < j1) {
+                if (j + u * kJoinWarps < j1) {
                     z[u][0] += x[u].x; z[u][1] += x[u].y; z[u][2] += x[u].z; z[u][3] += x[u].w;
                 }
         }
         #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t r = (int64_t)tr * ROWS + j + u * kEpiWarps;
-            if (j + u * kEpiWarps < j1 && r < a.R && n > 0) {
+            const int64_t r = (int64_t)tr * ROWS + j + u * kJoinWarps;
+            if (j + u * kJoinWarps < j1 && r < a.R && n > 0) {
                 finish<4>(a, z[u], r, c, n);
                 store_row<4>(a, z[u], r, c, n);
             }
@@ -698,10 +723,10 @@ __device__ __forceinline__ void join(const Args& a, const Work& w, uint32_t ring
 // Lanes are columns c of C, accumulator columns its rows.  Grid: a cluster of `split` CTAs per
 // tile of 128 c; the parts of the sum meet in shared memory and are added in rank order.
 template <int BN>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(Cfg<1, BN>::kThreads, 2)
 k_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a) {
     using F = Cfg<1, BN>;
-    constexpr int ST = F::kStages, H = F::kHalf, E = H < 16 ? H : 16;
+    constexpr int ST = F::kStages, H = F::kCol, E = H < 16 ? H : 16;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<ST> sm;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -710,9 +735,9 @@ k_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensor
     const uint32_t tmem = start<1, BN, ST>(sm, warp);
     int tc, tr;
     tile_at(a, w.first, tc, tr);
-    if (warp == kEpiWarps) {
+    if (warp == F::kEpi) {
         produce<1, BN, false, ST>(&tm_a, &tm_b, a, w, sm, ring);
-    } else if (warp == kEpiWarps + 1) {
+    } else if (warp == F::kEpi + 1) {
         issue<1, BN, ST>(a, w, sm, ring, tmem);
     } else {
         const int q = warp & 3, half = warp >> 2;
@@ -747,66 +772,104 @@ k_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensor
     if (a.split > 1) {
         __syncwarp();
         cluster_sync();
-        if (warp < kEpiWarps) join<BN, 128>(a, w, ring, warp, lane, tc, tr);
+        if (warp < F::kEpi) join<BN, 128>(a, w, ring, warp, lane, tc, tr);
         __syncwarp();
         cluster_sync();                    // no CTA's memory goes while another reads it
     }
     finish_cta<1, BN>(tmem, warp);
 }
 
-constexpr int kStageOut = 4096;            // outgoing: 32 rows of 128 bytes, two of them per epilogue warp
-// bf16 columns of an outgoing piece: a warp's BN / 2 columns in rows of 128 bytes, or of 64 where
-// they are no multiple of that.  (fp32 pieces are 32 columns, 128 bytes.)
-template <int BN>
-__host__ __device__ constexpr int out_piece() { return BN % 128 == 0 ? 64 : 32; }
-// Chunk c (of 4) of row r in 64-byte rows swizzled by TMA's 64-byte mode.
-__device__ __forceinline__ uint32_t swz64(int r, int c) { return (uint32_t)r * 64u + (uint32_t)((c ^ ((r >> 1) & 3)) << 4); }
+constexpr int kStageOut = 4096;            // an epilogue warp's outgoing 32 rows of 128 bytes
 template <int CG, int BN>
-constexpr int tile_smem() { return Cfg<CG, BN>::kRing + (CG == 2 ? 2 * kEpiWarps * kStageOut : 0) + 1024; }
+constexpr int tile_smem() { return Cfg<CG, BN>::kRing + (CG == 2 ? Cfg<CG, BN>::kEpi * kStageOut : 0) + 1024; }
 constexpr int kPartPitch = 132;            // floats per row of a part (CG 1): rows start 4 banks apart
 
 // Lanes are rows of C.  Grid: pairs (CG 2) walk the tiles; or a cluster of `split` CTAs per tile.
-template <int CG, int BN>
-__global__ void __launch_bounds__(kThreads, 1)
+// DIRECT: the contraction has several chunks and the results need no more than bias and residual
+// (no activation, no kept z, rows that leave by TMA).  The registers' sums then start from bias
+// and residual, read while the first chunk runs, and leave from the registers, and the last
+// accumulator is handed back as soon as it is added: with the residual read after the last chunk
+// that held its accumulator longer than the next chunk lasted (783 cycles per stage instead of
+// 520 with an fp32 residual).  Other sums go back to the last chunk's columns and leave from there
+// like a single chunk's.
+template <int CG, int BN, bool DIRECT>
+__global__ void __launch_bounds__(Cfg<CG, BN>::kThreads, 1)
 k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
        const __grid_constant__ CUtensorMap tm_y, const Args a) {
     using F = Cfg<CG, BN>;
-    constexpr int ST = F::kStages, H = F::kHalf, P = out_piece<BN>();
+    constexpr int ST = F::kStages, H = F::kCol;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<ST> sm;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const Work w = work_of<CG>(a);
     const uint32_t tmem = start<CG, BN, ST>(sm, warp);
-    if (warp == kEpiWarps) {
+    if (warp == F::kEpi) {
         produce<CG, BN, true, ST>(&tm_a, &tm_b, a, w, sm, ring);
-    } else if (warp == kEpiWarps + 1) {
+    } else if (warp == F::kEpi + 1) {
         if (CG == 1 || w.rank == 0) issue<CG, BN, ST>(a, w, sm, ring, tmem);
     } else {
         const int q = warp & 3, half = warp >> 2;
         const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + half * H;
-        const uint32_t stages = ring + F::kRing + warp * 2 * kStageOut;
-        uint32_t flip = 0;
+        const uint32_t stage = ring + F::kRing + warp * kStageOut;
         const bool parts = CG == 1 && a.split > 1;
         int ac = 0;
         bool ok = true;
+        // 32 columns from c on (e of the warp's), finished, into the outgoing stage; a full row of it leaves
+        auto send = [&](int e, int c, int64_t r0, const float* z) {
+            // 32 columns are a whole row of the stage, or half of one of 64 bf16
+            const bool begin = a.y.f32 || !(e & 32), end = a.y.f32 || (e & 32) || c + 32 >= a.C;
+            if (begin) {
+                if (lane == 0) bulk_wait_read0();              // the stage's last store has read it
+                __syncwarp();
+            }
+            if (a.y.f32) {
+                #pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    st_shared_v4(stage + swz128(lane, k), __float_as_uint(z[4 * k]), __float_as_uint(z[4 * k + 1]),
+                                 __float_as_uint(z[4 * k + 2]), __float_as_uint(z[4 * k + 3]));
+            } else {
+                #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    st_shared_v4(stage + swz128(lane, (e & 32) / 8 + k), pack_bf16(z[8 * k], z[8 * k + 1]), pack_bf16(z[8 * k + 2], z[8 * k + 3]),
+                                 pack_bf16(z[8 * k + 4], z[8 * k + 5]), pack_bf16(z[8 * k + 6], z[8 * k + 7]));
+            }
+            if (end) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    // what lies outside C is not written
+                    const int cs = a.y.f32 ? c : c & ~63;
+                    const int zh = a.y.hd ? cs / a.y.hd : 0;
+                    tma_store_3d(&tm_y, stage, cs - zh * a.y.hd, (int)r0, zh);
+                    bulk_commit();
+                }
+            }
+        };
         for (int t = w.first; ok && t < w.ntiles; t += w.step) {
             int tc, tr;
             tile_at(a, t, tc, tr);
             const int64_t r0 = (int64_t)tr * F::kM + (CG == 2 ? 128 * (int)w.rank : 0) + q * 32;
             const int c0 = tc * BN + half * H;
             int buf = ac & 1;
-            if (w.nch > 1 || parts) {
-                // the chunks add up in registers; the sum goes back to the last one's columns
+            if (DIRECT || w.nch > 1 || parts) {
+                // the chunks add up in registers
                 float v[H];
+                if (DIRECT) first_sums<H>(a, v, r0 + lane, c0);
                 for (int ch = 0; ch < w.nch; ++ch, ++ac) {
                     buf = ac & 1;
                     if (!warp_wait(&sm.acc_full[buf], (ac / 2) & 1, a.err, 3301)) { ok = false; break; }
                     tc_fence_after();
-                    add_columns<H>(at0 + buf * BN, v, ch == 0);
-                    if (ch < w.nch - 1) release<CG>(sm, buf, lane);
+                    add_columns<H>(at0 + buf * BN, v, ch == 0 && !DIRECT);
+                    if (DIRECT || ch < w.nch - 1) release<CG>(sm, buf, lane);
                 }
                 if (!ok) break;
+                if (DIRECT) {
+                    #pragma unroll
+                    for (int e = 0; e < H; e += 32)
+                        if (c0 + e < a.C) send(e, c0 + e, r0, v + e);
+                    continue;
+                }
                 if (parts) {
                     // row by row into the stages' memory, free since this tile is the block's only one
                     float* part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));
@@ -817,6 +880,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                     release<CG>(sm, buf, lane);
                     break;
                 }
+                // the sum goes back to the last chunk's columns
                 #pragma unroll
                 for (int i = 0; i < H / 8; ++i) Cols<8>::store(at0 + buf * BN + i * 8, v + i * 8);
                 tmem_wait_st();
@@ -838,42 +902,8 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
                 finish<32>(a, z, r0 + lane, c, n);
-                if (CG == 2 && a.y_tma) {
-                    // 32 columns are a whole row of the stage, or half of one of 64 bf16
-                    const bool wide = P == 64 && !a.y.f32;
-                    const bool begin = !wide || !(e & 32), end = !wide || (e & 32) || c + 32 >= a.C;
-                    if (begin) {
-                        flip ^= kStageOut;                     // the other stage,
-                        if (lane == 0) bulk_wait_read1();      // once its last store has read it
-                        __syncwarp();
-                    }
-                    const uint32_t stage = stages + flip;
-                    if (a.y.f32) {
-                        #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            st_shared_v4(stage + swz128(lane, k), __float_as_uint(z[4 * k]), __float_as_uint(z[4 * k + 1]),
-                                         __float_as_uint(z[4 * k + 2]), __float_as_uint(z[4 * k + 3]));
-                    } else {
-                        #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            st_shared_v4(stage + (P == 64 ? swz128(lane, (e & 32) / 8 + k) : swz64(lane, k)),
-                                         pack_bf16(z[8 * k], z[8 * k + 1]), pack_bf16(z[8 * k + 2], z[8 * k + 3]),
-                                         pack_bf16(z[8 * k + 4], z[8 * k + 5]), pack_bf16(z[8 * k + 6], z[8 * k + 7]));
-                    }
-                    if (end) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            // what lies outside C is not written
-                            const int cs = wide ? c & ~63 : c;
-                            const int zh = a.y.hd ? cs / a.y.hd : 0;
-                            tma_store_3d(&tm_y, stage, cs - zh * a.y.hd, (int)r0, zh);
-                            bulk_commit();
-                        }
-                    }
-                } else {
-                    store_row<32>(a, z, r0 + lane, c, n);
-                }
+                if (CG == 2 && a.y_tma) send(e, c, r0, z);
+                else store_row<32>(a, z, r0 + lane, c, n);
                 __syncwarp();
             }
             if (c0 >= a.C) release<CG>(sm, buf, lane);         // (a tile's half without columns)
@@ -883,7 +913,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
     if (CG == 1 && a.split > 1) {
         __syncwarp();
         cluster_sync();
-        if (warp < kEpiWarps) {
+        if (warp < F::kEpi) {
             int tc, tr;
             tile_at(a, w.first, tc, tr);
             join<128, kPartPitch>(a, w, ring, warp, lane, tc, tr);
@@ -1054,19 +1084,17 @@ static int make_operand(CUtensorMap* m, Operand* o, const Matrix& x, bool mn, in
     return r == CUDA_SUCCESS ? PRISM_OK : PRISM_ERR_CUDA;
 }
 
-// C as boxes of 32 rows by 128 bytes (64 bytes: bf16 pieces of 32 columns).
-static int make_out_map(CUtensorMap* m, const Out& y, int64_t R, int C, int piece) {
+// C as boxes of 32 rows by 128 bytes.
+static int make_out_map(CUtensorMap* m, const Out& y, int64_t R, int C) {
     auto enc = encode_fn();
     if (!enc) return PRISM_ERR_CUDA;
     const int e = y.f32 ? 4 : 2;
     cuuint64_t dims[3] = {(cuuint64_t)(y.hd ? y.hd : C), (cuuint64_t)R, (cuuint64_t)(y.hd ? C / y.hd : 1)};
     cuuint64_t strides[2] = {(cuuint64_t)y.rs * e, (cuuint64_t)(y.hd ? y.hs : R * y.rs) * e};
-    const bool half = !y.f32 && piece == 32;
-    cuuint32_t boxd[3] = {(cuuint32_t)(y.f32 ? 32 : piece), 32, 1};
+    cuuint32_t boxd[3] = {(cuuint32_t)(128 / e), 32, 1};
     cuuint32_t es[3] = {1, 1, 1};
     CUresult r = enc(m, y.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, y.p, dims, strides,
-                     boxd, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                     boxd, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PRISM_OK : PRISM_ERR_CUDA;
 }
@@ -1081,10 +1109,11 @@ struct Shape {
 // The tile of a product of R rows, C columns and kb stages.
 //   up to 64 rows: k_few, its contraction split until two CTAs run on every SM.
 //   else the least of the estimates, in cycles of one SM:
-//     pairs on 256 x bn tiles: their waves over 74 pairs, each kb stages of 2.03 bn cycles (measured:
-//       518 at 256; the instruction's own 512) and 2,500 to fill and drain; 8,000 to start;
-//     single CTAs on 128 x 128 tiles, `split` to a tile: all at once, kb / split stages of 300 cycles,
-//       10,000 to start and 4,000 to join the parts.
+//     pairs on 256 x bn tiles: their waves over 74 pairs, each kb stages of 522, 430 or 310 cycles
+//       (measured; the instructions' own 512, 384 and 256: narrower tiles load more bytes per
+//       product) and 2,500 to fill and drain; 8,000 to start;
+//     single CTAs on 128 x 128 tiles, `split` to a tile: all at once, kb / split stages of 460 cycles
+//       (32 KB each to one SM), 10,000 to start and 4,000 to join the parts.
 //   A tile width that fits the waves counts most: 512 rows of 5,120 by 5,120 are 80 tiles at bn = 128
 //   (two waves, 31.8 us), 40 at 256 (half of the pairs idle, 30.6 us), 54 at 192.
 static Shape shape_of(int64_t R, int64_t C, int kb, bool x_mn, bool y_mn) {
@@ -1100,13 +1129,13 @@ static Shape shape_of(int64_t R, int64_t C, int kb, bool x_mn, bool y_mn) {
     for (int bn : {256, 192, 128}) {
         if (bn == 192 && y_mn) continue;                         // a CTA's half is no whole slabs
         const int64_t waves = ceil_div(ceil_div(R, 256) * ceil_div(C, bn), 74);
-        const int64_t t = 8000 + waves * ((int64_t)kb * bn * 65 / 32 + 2500);
+        const int64_t t = 8000 + waves * ((int64_t)kb * (bn == 256 ? 522 : bn == 192 ? 430 : 310) + 2500);
         if (t < least) { least = t; best = Shape{0, 2, bn, 1}; }
     }
     const int64_t tiles = ceil_div(R, 128) * ceil_div(C, 128);
     for (int split : {1, 2, 4, 8}) {
         if (tiles * split > 148 || (split > 1 && kb < 4 * split)) break;
-        const int64_t t = 10000 + ceil_div(kb, split) * 300 + (split > 1 ? 4000 : 0);
+        const int64_t t = 10000 + ceil_div(kb, split) * 460 + (split > 1 ? 4000 : 0);
         if (t < least) { least = t; best = Shape{0, 1, 128, split}; }
     }
     return best;
@@ -1115,11 +1144,11 @@ static Shape shape_of(int64_t R, int64_t C, int kb, bool x_mn, bool y_mn) {
 // Starts `kernel` as clusters of `group` CTAs.  The shared-memory opt-in is made for every call:
 // it belongs to the device that is current.
 template <typename... P, typename... A>
-static int start_kernel(void (*kernel)(P...), int64_t ctas, int group, int smem, cudaStream_t s, const A&... args) {
+static int start_kernel(void (*kernel)(P...), int64_t ctas, int group, int threads, int smem, cudaStream_t s, const A&... args) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return PRISM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -1135,12 +1164,14 @@ static int start_kernel(void (*kernel)(P...), int64_t ctas, int group, int smem,
 template <int CG, int BN>
 static int launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty, const Args& a, cudaStream_t s) {
     const int64_t tiles = (int64_t)a.tiles_c * a.tiles_r;
-    return start_kernel(k_tile<CG, BN>, CG == 2 ? 2 * (tiles < 74 ? tiles : 74) : tiles * a.split, CG == 2 ? 2 : a.split,
-                        tile_smem<CG, BN>(), s, ta, tb, ty, a);
+    const bool direct = CG == 2 && a.kblocks > a.chunk && a.y_tma && a.act == PRISM_ACT_NONE && !a.pre.p;
+    return start_kernel(direct ? k_tile<CG, BN, CG == 2> : k_tile<CG, BN, false>, CG == 2 ? 2 * (tiles < 74 ? tiles : 74) : tiles * a.split, CG == 2 ? 2 : a.split,
+                        Cfg<CG, BN>::kThreads, tile_smem<CG, BN>(), s, ta, tb, ty, a);
 }
 template <int BN>
 static int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const Args& a, cudaStream_t s) {
-    return start_kernel(k_few<BN>, (int64_t)a.tiles_c * a.tiles_r * a.split, a.split, Cfg<1, BN>::kRing + 1024, s, ta, tb, a);
+    return start_kernel(k_few<BN>, (int64_t)a.tiles_c * a.tiles_r * a.split, a.split, Cfg<1, BN>::kThreads,
+                        Cfg<1, BN>::kRing + 1024, s, ta, tb, a);
 }
 
 // C[r][c] = sum_k X[r][k] Y[c][k]; K the contraction's length, x_mn / y_mn: the matrix's rows are k.
@@ -1170,7 +1201,7 @@ static int product(const Matrix& X, bool x_mn, const Matrix& Y, bool y_mn, int64
     // a map of C wants its address and row stride in whole 16 bytes
     CUtensorMap to{};
     a.y_tma = sh.cg == 2 && a.y.vec;
-    if (a.y_tma) st = make_out_map(&to, a.y, R, C, sh.bn % 128 == 0 ? 64 : 32);
+    if (a.y_tma) st = make_out_map(&to, a.y, R, C);
     if (st) return st;
     if (sh.cg == 1) return launch_tile<1, 128>(tx, ty, to, a, s);
     return sh.bn == 256   ? launch_tile<2, 256>(tx, ty, to, a, s)
