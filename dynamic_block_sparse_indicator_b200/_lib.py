@@ -599,6 +599,7 @@ class _Launch:
         return t
 
     def check(self, status, what):
+        """Raises on a status; a call on another stream marks the given tensors as used there."""
         if status:
             raise PrismError(status, what)
         if self.other:
@@ -785,6 +786,12 @@ def _size(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
+def _check_status(t):
+    import torch
+    if t is not None and (t.dtype != torch.int32 or t.numel() < 4 or not t.is_contiguous()):
+        raise ValueError("status must be four contiguous int32")
+
+
 def linear(x, W, bias=None, residual=None, activation=PRISM_ACT_NONE, y=None, out_dtype=None, out_heads=0, pre=None,
            want_pre=False, workspace=None, status=None, stream=None):
     """(y, pre, status): y = act(x W^T + bias) + residual.  x is bf16 rows [M, K] (any row stride) or
@@ -818,6 +825,7 @@ def linear(x, W, bias=None, residual=None, activation=PRISM_ACT_NONE, y=None, ou
         raise ValueError(f"bias must be [{N}]")
     p = PrismLinearParams(M, K, N, in_heads, out_heads, int(activation), _code(out_dtype, "y"),
                           PRISM_F32 if bias is None else _code(bias.dtype, "bias"), PRISM_F32, xs, ws_, strides[0], strides[1])
+    _check_status(status)
     lib = load()
     with _Launch([x, W, bias, residual, y, pre, workspace, status], stream) as go:
         y = go.empty(want, out_dtype) if y is None else y
@@ -857,6 +865,7 @@ def linear_bwd(dy, x, W, pre=None, activation=PRISM_ACT_NONE, dx=None, dW=None, 
             raise ValueError(f"{what} must be a contiguous {dtype} {shape}")
     p = PrismLinearParams(M, K, N, in_heads, out_heads, int(activation), _code(dy.dtype, "dy"), PRISM_F32,
                           _code(dw_dtype, "dW"), xs, ws_, ys, N)
+    _check_status(status)
     lib = load()
     with _Launch([dy, x, W, pre, dx, dW, db, workspace, status], stream) as go:
         dx = go.empty(x.shape, torch.bfloat16) if dx is None and want_dx else dx

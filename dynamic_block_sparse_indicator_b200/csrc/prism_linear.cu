@@ -14,9 +14,7 @@
 // Two kernels:
 //   k_tile  many rows: TMEM lanes are rows, columns are c.  A pair of CTAs (cta_group::2)
 //           shares a 256 x BN tile, or one CTA has 128 x 128, whose contraction a cluster may
-//           split.  A pair's results leave through 4 KB stages and TMA stores; a single CTA's
-//           straight from the registers (its shared memory holds a deep ring instead: few CTAs
-//           have to cover the latency).
+//           split.  A warp's results leave through a 4 KB stage and TMA stores.
 //   k_few   up to 64 rows: TMEM lanes are c and columns are rows, so few tokens are a small
 //           N of the instruction instead of an M tile of padding.  Bound by HBM's read of W;
 //           a cluster splits the contraction.
@@ -71,7 +69,7 @@ struct Args {
     int chunk;                             // stages per accumulation chunk
     int tiles_c, tiles_r, band;
     Out y, pre, res;
-    int y_tma;                             // the results' rows can leave by TMA
+    int fast;                              // results leave by TMA; residual and kept z in 16-byte accesses
     const void* bias;
     int bias_f32, act;
     int* err;
@@ -213,9 +211,22 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
 // one quotient.
 __device__ __forceinline__ float logistic(float t) { return __fdividef(1.f, 1.f + __expf(-t)); }
 __device__ __forceinline__ float tanh_arg(float z) { return 1.5957691216057308f * (z + 0.044715f * z * z * z); }
+// The normal distribution's Phi(z), and e^(-z^2 / 2) for its density: Abramowitz and Stegun's
+// formula 7.1.26 for erfc(x), x = |z| / sqrt 2, t = 1 / (1 + p x), a polynomial of degree 5 in t
+// times e^(-x^2), within 1.5e-7; the gradient wants that power too.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+    const float x = fabsf(z) * 0.70710678118654752f;
+    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+    e = __expf(-x * x);
+    const float q = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                             0.254829592f);
+    const float tail = 0.5f * q * e;
+    return z > 0.f ? 1.f - tail : tail;
+}
 __device__ __forceinline__ float act_of(float z, int act) {
+    float e;
     switch (act) {
-        case PRISM_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+        case PRISM_ACT_GELU: return z * normal_cdf(z, e);
         case PRISM_ACT_GELU_TANH: return z * logistic(tanh_arg(z));
         case PRISM_ACT_SILU: return z * logistic(z);
         default: return z;
@@ -223,8 +234,11 @@ __device__ __forceinline__ float act_of(float z, int act) {
 }
 __device__ __forceinline__ float act_grad(float z, int act) {
     switch (act) {
-        case PRISM_ACT_GELU:
-            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+        case PRISM_ACT_GELU: {
+            float e;
+            const float p = normal_cdf(z, e);
+            return p + z * e * 0.39894228040143268f;
+        }
         case PRISM_ACT_GELU_TANH: {
             const float s = logistic(tanh_arg(z));
             return s + z * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z * z);
@@ -463,12 +477,17 @@ __device__ __forceinline__ void produce(const void* tm_a, const void* tm_b, cons
             if (++s == ST) { s = 0; ++round; }
         }
     }
-    // every copy has landed before the block may end (an MMA issuer that gave up waits for none)
-    if (CG == 1 || w.rank == 0)
+    // every copy has landed before the block may end: after a wait that gave up, too (then for at
+    // most a tenth of a second)
+    if (CG == 1 || w.rank == 0) {
+        const uint64_t t0 = globaltimer_ns();
         for (int i = 0; i < ST; ++i) {
             const int uses = round + (i < s ? 1 : 0);
-            if (uses && !warp_wait(&sm.full[i], (uses - 1) & 1, a.err, 3102)) break;
+            if (uses)
+                while (!mbar_try(&sm.full[i], (uses - 1) & 1) && globaltimer_ns() - t0 < kWaitNs / 10) {}
         }
+        __syncwarp();
+    }
 }
 
 // The MMA issuer (one warp; of a pair, the first CTA's).
@@ -670,6 +689,11 @@ __device__ __forceinline__ void store_row(const Args& a, const float* z, int64_t
         }
     }
 }
+__device__ __forceinline__ float ld_shared_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int32_t x, int32_t y, int32_t z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
                  :: "l"(reinterpret_cast<uint64_t>(tmap)), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
@@ -781,18 +805,21 @@ k_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensor
 
 constexpr int kStageOut = 4096;            // an epilogue warp's outgoing 32 rows of 128 bytes
 template <int CG, int BN>
-constexpr int tile_smem() { return Cfg<CG, BN>::kRing + (CG == 2 ? Cfg<CG, BN>::kEpi * kStageOut : 0) + 1024; }
+constexpr int tile_smem() { return Cfg<CG, BN>::kRing + Cfg<CG, BN>::kEpi * kStageOut + 1024; }
 constexpr int kPartPitch = 132;            // floats per row of a part (CG 1): rows start 4 banks apart
 
 // Lanes are rows of C.  Grid: pairs (CG 2) walk the tiles; or a cluster of `split` CTAs per tile.
-// DIRECT: the contraction has several chunks and the results need no more than bias and residual
-// (no activation, no kept z, rows that leave by TMA).  The registers' sums then start from bias
-// and residual, read while the first chunk runs, and leave from the registers, and the last
-// accumulator is handed back as soon as it is added: with the residual read after the last chunk
-// that held its accumulator longer than the next chunk lasted (783 cycles per stage instead of
-// 520 with an fp32 residual).  Other sums go back to the last chunk's columns and leave from there
-// like a single chunk's.
-template <int CG, int BN, bool DIRECT>
+// Three epilogues, so that each keeps its registers:
+//   kSingle  one chunk, rows at 16-byte alignment: straight from the accumulator's columns.
+//   kDirect  several chunks, no activation, no kept z, the same alignment.  The registers' sums
+//            start from bias and residual, read while the first chunk runs, and leave from the
+//            registers, and the last accumulator is handed back as soon as it is added: with the
+//            residual read after the last chunk that held its accumulator longer than the next
+//            chunk lasted (783 cycles per stage instead of 628 with an fp32 residual).
+//   kGeneral the rest: sums of chunks go back to the last one's columns and leave from there; rows
+//            of any alignment; single CTAs.
+constexpr int kSingle = 0, kDirect = 1, kGeneral = 2;
+template <int CG, int BN, int MODE>
 __global__ void __launch_bounds__(Cfg<CG, BN>::kThreads, 1)
 k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
        const __grid_constant__ CUtensorMap tm_y, const Args a) {
@@ -812,6 +839,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
         const int q = warp & 3, half = warp >> 2;
         const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + half * H;
         const uint32_t stage = ring + F::kRing + warp * kStageOut;
+        constexpr bool DIRECT = MODE == kDirect;
         const bool parts = CG == 1 && a.split > 1;
         int ac = 0;
         bool ok = true;
@@ -852,7 +880,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
             const int64_t r0 = (int64_t)tr * F::kM + (CG == 2 ? 128 * (int)w.rank : 0) + q * 32;
             const int c0 = tc * BN + half * H;
             int buf = ac & 1;
-            if (DIRECT || w.nch > 1 || parts) {
+            if (DIRECT || (MODE == kGeneral && (w.nch > 1 || parts))) {
                 // the chunks add up in registers
                 float v[H];
                 if (DIRECT) first_sums<H>(a, v, r0 + lane, c0);
@@ -901,14 +929,34 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                 float z[32];
                 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
-                finish<32>(a, z, r0 + lane, c, n);
-                if (CG == 2 && a.y_tma) send(e, c, r0, z);
-                else store_row<32>(a, z, r0 + lane, c, n);
-                __syncwarp();
+                if (MODE != kGeneral || a.fast) {
+                    finish<32>(a, z, r0 + lane, c, n);
+                    send(e, c, r0, z);
+                    __syncwarp();
+                } else {
+                    // rows at any alignment: turned in the stage, so that a row's columns lie in the lanes
+                    // (a lane writing along its own row took 7.1 ms where this takes 2.1, 24,743 rows of
+                    // 1,904 by 13,119)
+                    #pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        st_shared_v4(stage + swz128(lane, k), u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+                    __syncwarp();
+                    const Lane l = lane_of(a, c + lane);
+                    #pragma unroll 1
+                    for (int j = 0; j < 32; j += 8) {
+                        const int64_t left = a.R - (r0 + j);
+                        if (left <= 0) break;
+                        float x[8];
+                        #pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = ld_shared_f32(stage + swz128(j + i, lane >> 2) + (lane & 3) * 4);
+                        emit<8>(a, l, r0 + j, left < 8 ? (int)left : 8, x);
+                    }
+                    __syncwarp();
+                }
             }
             if (c0 >= a.C) release<CG>(sm, buf, lane);         // (a tile's half without columns)
         }
-        if (CG == 2 && lane == 0) bulk_wait0();
+        if (lane == 0) bulk_wait0();
     }
     if (CG == 1 && a.split > 1) {
         __syncwarp();
@@ -925,17 +973,101 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
 }
 
 // ------------------------------------------------- elementwise passes
-// Rows [M][K] whose address or stride a TMA map cannot take (K or the stride not a multiple
-// of 8 elements), copied to a padded stride in the workspace.
+// Eight bf16 from element `at` on of a tensor of `total` elements at a 16-byte aligned address,
+// at any offset: the one or two aligned 16-byte words that hold them, shifted together.  (The
+// second word is read only where all of it lies in the tensor.)
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16* base, int64_t at, int64_t total) {
+    const int64_t a = at & ~int64_t(7);
+    const int o = (int)(at & 7);
+    const uint4 lo = __ldg(reinterpret_cast<const uint4*>(base + a));
+    if (o == 0) return lo;
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, 0, 0, 0, 0};
+    if (a + 16 <= total) {
+        const uint4 hi = __ldg(reinterpret_cast<const uint4*>(base + a + 8));
+        w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
+    } else {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(base + a + 8);
+        #pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < o) w[4 + i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+    }
+    if (o & 4) {
+        #pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (o & 2) {
+        #pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (o & 1) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void unpack8(const uint4& x, float* f) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(u[e] << 16);
+        f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+    }
+}
+// Row r's columns c .. c + 7 of a tensor as fp32; columns from N on read as zeros.
+__device__ __forceinline__ void read8(const Out& o, int64_t off, int64_t r, int c, int N, int64_t total, float* f) {
+    const int64_t at0 = off + r * o.rs;
+    const int n = min(8, N - c);
+    if (o.f32) {
+        const float* p = static_cast<const float*>(o.p) + at0;
+        if (o.vec && n == 8) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(p)), y = __ldg(reinterpret_cast<const float4*>(p) + 1);
+            f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+            f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+        } else {
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = e < n ? __ldg(p + e) : 0.f;
+        }
+    } else {
+        const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(o.p);
+        if (n == 8) {
+            unpack8(load8(b, at0, total), f);
+        } else {
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = e < n ? __bfloat162float(b[at0 + e]) : 0.f;
+        }
+    }
+}
+
+// Rows [rows][K] whose stride a TMA map cannot take (no multiple of 8 elements), copied to a
+// padded stride in the workspace (the padding is zero).
 __global__ void __launch_bounds__(256) k_pack(const __nv_bfloat16* src, int64_t stride, int64_t rows, int K,
-                                              __nv_bfloat16* dst, int64_t dstride) {
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int c = threadIdx.x; c < K; c += blockDim.x) dst[r * dstride + c] = src[r * stride + c];
+                                              __nv_bfloat16* dst, int groups) {
+    const int64_t total = (rows - 1) * stride + K;
+    // a block takes one row's groups at a time, or several short rows
+    const int per = groups < 256 ? 256 / groups : 1;
+    const int sub = groups < 256 ? threadIdx.x / groups : 0, g0 = groups < 256 ? threadIdx.x - sub * groups : threadIdx.x;
+    if (sub >= per) return;
+    for (int64_t r = (int64_t)blockIdx.x * per + sub; r < rows; r += (int64_t)gridDim.x * per)
+        for (int g = g0; g < groups; g += 256) {
+            const int c = g * 8;
+            uint4 x;
+            if (c + 8 <= K) {
+                x = load8(src, r * stride + c, total);
+            } else {
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(src + r * stride + c);
+                uint32_t w[4] = {0, 0, 0, 0};
+                #pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < K) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+                x = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            reinterpret_cast<uint4*>(dst)[r * groups + g] = x;
+        }
 }
 
 struct DzArgs {
     Out dy, pre;                           // pre.p null: no activation
-    int64_t M;
+    int64_t M, dy_total, pre_total;        // elements of the tensors
     int N, act;
     __nv_bfloat16* dz;                     // [M][dzs], or null (dy itself feeds the products)
     int64_t dzs;
@@ -943,79 +1075,108 @@ struct DzArgs {
     int64_t rows;                          // rows of a chunk
 };
 
+// A row's eight values as they are loaded, so that several rows' loads are in flight before the
+// first is used.  VEC: the tensor's rows lie at 16-byte alignment.
+template <bool VEC, bool F32> struct Raw8;
+template <> struct Raw8<true, false> {
+    uint4 x;
+    __device__ __forceinline__ void load(const Out& o, int64_t at, int64_t) {
+        x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(o.p) + at));
+    }
+    __device__ __forceinline__ void get(float* f) const { unpack8(x, f); }
+};
+template <> struct Raw8<false, false> {
+    uint4 x;
+    __device__ __forceinline__ void load(const Out& o, int64_t at, int64_t total) {
+        x = load8(static_cast<const __nv_bfloat16*>(o.p), at, total);
+    }
+    __device__ __forceinline__ void get(float* f) const { unpack8(x, f); }
+};
+template <> struct Raw8<true, true> {
+    float4 x, y;
+    __device__ __forceinline__ void load(const Out& o, int64_t at, int64_t) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(o.p) + at);
+        x = __ldg(p);
+        y = __ldg(p + 1);
+    }
+    __device__ __forceinline__ void get(float* f) const {
+        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+        f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+    }
+};
+template <> struct Raw8<false, true> {
+    float x[8];
+    __device__ __forceinline__ void load(const Out& o, int64_t at, int64_t) {
+        const float* p = static_cast<const float*>(o.p) + at;
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __ldg(p + e);
+    }
+    __device__ __forceinline__ void get(float* f) const {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = x[e];
+    }
+};
+
 // dz = dy act'(z) rounded to the products' 16 bits, and its column sums (of the unrounded
-// values): a block takes 32 V columns of a chunk of rows, 8 rows at a time, and adds its
-// sums in a fixed order.  HBM-bound: one read of dy (and z), one write of dz.
-template <int V>
-__global__ void __launch_bounds__(256) k_dz(const DzArgs a) {
-    __shared__ float sm[8][32 * V + 1];
+// values): a block takes 256 columns of a chunk of rows, 8 rows at a time and U of those loaded
+// ahead, and adds its sums in a fixed order.  HBM-bound: one read of dy (and z), one write of dz.
+template <bool VEC, bool F32, int ACT>
+__global__ void __launch_bounds__(256, 4) k_dz(const DzArgs a) {
+    constexpr int U = ACT ? 2 : 4;             // rows loaded ahead
+    __shared__ float sm[8][256 + 8];
     const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
-    const int c = (blockIdx.x * 32 + cl) * V;
+    const int c = (blockIdx.x * 32 + cl) * 8;
     const int64_t r1 = min(a.M, (int64_t)(blockIdx.y + 1) * a.rows);
-    float sum[V];
+    float sum[8];
     #pragma unroll
-    for (int e = 0; e < V; ++e) sum[e] = 0.f;
+    for (int e = 0; e < 8; ++e) sum[e] = 0.f;
     if (c < a.N) {
-        const int64_t dyo = at(a.dy, c), preo = a.pre.p ? at(a.pre, c) : 0;
-        #pragma unroll 4
-        for (int64_t r = (int64_t)blockIdx.y * a.rows + rl; r < r1; r += 8) {
-            float g[V], z[V];
-            if (V == 8) {
-                if (a.dy.f32) {
-                    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.dy.p) + dyo + r * a.dy.rs);
-                    const float4 x = __ldcs(p), y = __ldcs(p + 1);
-                    g[0] = x.x; g[1 % V] = x.y; g[2 % V] = x.z; g[3 % V] = x.w;
-                    g[4 % V] = y.x; g[5 % V] = y.y; g[6 % V] = y.z; g[7 % V] = y.w;
-                } else {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dy.p) + dyo + r * a.dy.rs));
-                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-                    #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        g[(2 * e) % V] = __uint_as_float(u[e] << 16);
-                        g[(2 * e + 1) % V] = __uint_as_float(u[e] & 0xffff0000u);
-                    }
-                }
-                if (a.pre.p) {
-                    const uint4 x = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.pre.p) + preo + r * a.pre.rs));
-                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-                    #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        z[(2 * e) % V] = __uint_as_float(u[e] << 16);
-                        z[(2 * e + 1) % V] = __uint_as_float(u[e] & 0xffff0000u);
-                    }
-                }
-            } else {
-                g[0] = a.dy.f32 ? static_cast<const float*>(a.dy.p)[dyo + r * a.dy.rs]
-                                : __bfloat162float(static_cast<const __nv_bfloat16*>(a.dy.p)[dyo + r * a.dy.rs]);
-                if (a.pre.p) z[0] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.pre.p)[preo + r * a.pre.rs]);
-            }
+        const int64_t dyo = at(a.dy, c), preo = ACT ? at(a.pre, c) : 0;
+        auto take = [&](float* g, const float* z, int64_t r) {
             #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (a.pre.p) g[e] *= act_grad(z[e], a.act);
+            for (int e = 0; e < 8; ++e) {
+                if (ACT) g[e] *= act_grad(z[e], ACT);
                 sum[e] += g[e];
             }
-            if (a.dz) {
-                if (V == 8)
-                    *reinterpret_cast<uint4*>(a.dz + r * a.dzs + c) =
-                        make_uint4(pack_bf16(g[0], g[1 % V]), pack_bf16(g[2 % V], g[3 % V]), pack_bf16(g[4 % V], g[5 % V]),
-                                   pack_bf16(g[6 % V], g[7 % V]));
-                else
-                    a.dz[r * a.dzs + c] = __float2bfloat16_rn(g[0]);
+            if (a.dz)      // (the padding behind N is zero)
+                *reinterpret_cast<uint4*>(a.dz + r * a.dzs + c) =
+                    make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7]));
+        };
+        int64_t r = (int64_t)blockIdx.y * a.rows + rl;
+        if (c + 8 <= a.N)
+            for (; r + 8 * (U - 1) < r1; r += 8 * U) {
+                Raw8<VEC, F32> g[U];
+                Raw8<VEC, false> z[U];
+                #pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    g[i].load(a.dy, dyo + (r + 8 * i) * a.dy.rs, a.dy_total);
+                    if (ACT) z[i].load(a.pre, preo + (r + 8 * i) * a.pre.rs, a.pre_total);
+                }
+                #pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    float x[8], y[8];
+                    g[i].get(x);
+                    if (ACT) z[i].get(y);
+                    take(x, y, r + 8 * i);
+                }
             }
+        for (; r < r1; r += 8) {
+            float x[8], y[8];
+            read8(a.dy, dyo, r, c, a.N, a.dy_total, x);
+            if (ACT) read8(a.pre, preo, r, c, a.N, a.pre_total, y);
+            take(x, y, r);
         }
     }
     if (!a.part) return;
     #pragma unroll
-    for (int e = 0; e < V; ++e) sm[rl][cl * V + e] = sum[e];
+    for (int e = 0; e < 8; ++e) sm[rl][cl * 8 + e] = sum[e];
     __syncthreads();
-    for (int i = threadIdx.x; i < 32 * V; i += 256) {
-        const int col = blockIdx.x * 32 * V + i;
-        if (col >= a.N) break;
-        float s = 0.f;
-        #pragma unroll
-        for (int k = 0; k < 8; ++k) s += sm[k][i];
-        a.part[(int64_t)blockIdx.y * a.N + col] = s;
-    }
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    if (col >= a.N) return;
+    float s = 0.f;
+    #pragma unroll
+    for (int k = 0; k < 8; ++k) s += sm[k][threadIdx.x];
+    a.part[(int64_t)blockIdx.y * a.N + col] = s;
 }
 
 // db: the chunks' sums in a fixed order, in 64 bits (a sum over every token: its parts cancel).
@@ -1164,8 +1325,12 @@ static int start_kernel(void (*kernel)(P...), int64_t ctas, int group, int threa
 template <int CG, int BN>
 static int launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty, const Args& a, cudaStream_t s) {
     const int64_t tiles = (int64_t)a.tiles_c * a.tiles_r;
-    const bool direct = CG == 2 && a.kblocks > a.chunk && a.y_tma && a.act == PRISM_ACT_NONE && !a.pre.p;
-    return start_kernel(direct ? k_tile<CG, BN, CG == 2> : k_tile<CG, BN, false>, CG == 2 ? 2 * (tiles < 74 ? tiles : 74) : tiles * a.split, CG == 2 ? 2 : a.split,
+    void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, Args) = k_tile<CG, BN, kGeneral>;
+    if constexpr (CG == 2) {
+        if (a.fast && a.kblocks <= a.chunk) kernel = k_tile<CG, BN, kSingle>;
+        else if (a.fast && a.act == PRISM_ACT_NONE && !a.pre.p) kernel = k_tile<CG, BN, kDirect>;
+    }
+    return start_kernel(kernel, CG == 2 ? 2 * (tiles < 74 ? tiles : 74) : tiles * a.split, CG == 2 ? 2 : a.split,
                         Cfg<CG, BN>::kThreads, tile_smem<CG, BN>(), s, ta, tb, ty, a);
 }
 template <int BN>
@@ -1200,8 +1365,8 @@ static int product(const Matrix& X, bool x_mn, const Matrix& Y, bool y_mn, int64
         return sh.bn == 16 ? launch_few<16>(ty, tx, a, s) : sh.bn == 32 ? launch_few<32>(ty, tx, a, s) : launch_few<64>(ty, tx, a, s);
     // a map of C wants its address and row stride in whole 16 bytes
     CUtensorMap to{};
-    a.y_tma = sh.cg == 2 && a.y.vec;
-    if (a.y_tma) st = make_out_map(&to, a.y, R, C);
+    a.fast = a.y.vec && (!a.res.p || a.res.vec) && (!a.pre.p || a.pre.vec);
+    if (a.fast) st = make_out_map(&to, a.y, R, C);
     if (st) return st;
     if (sh.cg == 1) return launch_tile<1, 128>(tx, ty, to, a, s);
     return sh.bn == 256   ? launch_tile<2, 256>(tx, ty, to, a, s)
@@ -1244,15 +1409,14 @@ static bool forms_dz(const prism_linear_params* p) {
 static size_t dz_bytes(const prism_linear_params* p) { return forms_dz(p) ? up256((size_t)p->M * pad8(p->N) * 2) : 0; }
 
 struct DzGrid {
-    int v, x, y;
+    int x, y;
     int64_t rows;
 };
-// Row chunks so that about eight blocks per SM run; a chunk has at least 64 rows.
+// Row chunks: two full rounds of four blocks per SM at most; a chunk has at least 64 rows.
 static DzGrid dz_grid(const prism_linear_params* p) {
     DzGrid g;
-    g.v = p->N % 8 == 0 && p->y_stride % 8 == 0 ? 8 : 1;
-    g.x = (int)ceil_div(p->N, 32 * g.v);
-    int64_t y = ceil_div(8 * 148, g.x);
+    g.x = (int)ceil_div(p->N, 256);
+    int64_t y = 8 * 148 / g.x;
     if (y > ceil_div(p->M, 64)) y = ceil_div(p->M, 64);
     if (y < 1) y = 1;
     g.rows = ceil_div(p->M > 0 ? p->M : 1, y);
@@ -1316,8 +1480,10 @@ static int operand(Matrix* m, const void* p, int64_t rows, int cols, int heads, 
     const int64_t ld = pad8(cols);
     auto* dst = reinterpret_cast<__nv_bfloat16*>(ws);
     ws += up256((size_t)rows * ld * 2);
-    k_pack<<<(unsigned)(rows < 148 * 8 ? rows : 148 * 8), 256, 0, s>>>(static_cast<const __nv_bfloat16*>(p), stride, rows, cols,
-                                                                       dst, ld);
+    const int groups = (int)(ld / 8), per = groups < 256 ? 256 / groups : 1;
+    const int64_t blocks = ceil_div(rows, per);
+    k_pack<<<(unsigned)(blocks < 148 * 32 ? blocks : 148 * 32), 256, 0, s>>>(static_cast<const __nv_bfloat16*>(p), stride, rows,
+                                                                            cols, dst, groups);
     *m = Matrix{dst, rows, cols, ld, 1};
     return cudaGetLastError() == cudaSuccess ? PRISM_OK : PRISM_ERR_CUDA;
 }
@@ -1338,6 +1504,21 @@ static int forward(const prism_linear_params* p, const void* x, const void* W, c
     a.act = p->activation;
     a.err = err;
     return product(mx, false, mw, false, p->M, p->N, p->K, a, s);
+}
+
+template <bool VEC, bool F32>
+static void launch_dz_of(const DzArgs& d, dim3 grid, cudaStream_t s) {
+    switch (d.pre.p ? d.act : PRISM_ACT_NONE) {
+        case PRISM_ACT_GELU: k_dz<VEC, F32, PRISM_ACT_GELU><<<grid, 256, 0, s>>>(d); break;
+        case PRISM_ACT_GELU_TANH: k_dz<VEC, F32, PRISM_ACT_GELU_TANH><<<grid, 256, 0, s>>>(d); break;
+        case PRISM_ACT_SILU: k_dz<VEC, F32, PRISM_ACT_SILU><<<grid, 256, 0, s>>>(d); break;
+        default: k_dz<VEC, F32, PRISM_ACT_NONE><<<grid, 256, 0, s>>>(d); break;
+    }
+}
+static void launch_dz(const DzArgs& d, dim3 grid, cudaStream_t s) {
+    const bool vec = d.dy.vec && d.N % 8 == 0;
+    if (vec) d.dy.f32 ? launch_dz_of<true, true>(d, grid, s) : launch_dz_of<true, false>(d, grid, s);
+    else d.dy.f32 ? launch_dz_of<false, true>(d, grid, s) : launch_dz_of<false, false>(d, grid, s);
 }
 
 static int backward(const prism_linear_params* p, const void* dy, const void* x, const void* W, const void* pre, void* dx,
@@ -1362,8 +1543,9 @@ static int backward(const prism_linear_params* p, const void* dy, const void* x,
         d.rows = g.rows;
         if (db) d.part = reinterpret_cast<float*>(ws);
         ws += up256((size_t)g.y * p->N * 4);
-        if (g.v == 8) k_dz<8><<<dim3(g.x, g.y), 256, 0, s>>>(d);
-        else k_dz<1><<<dim3(g.x, g.y), 256, 0, s>>>(d);
+        d.dy_total = p->out_heads ? p->M * p->N : (p->M - 1) * p->y_stride + p->N;
+        d.pre_total = p->M * p->N;
+        launch_dz(d, dim3(g.x, g.y), s);
         if (db) k_db<<<(unsigned)ceil_div(p->N, 32), 256, 0, s>>>(d.part, g.y, p->N, db);
         if (cudaGetLastError() != cudaSuccess) return PRISM_ERR_CUDA;
     }

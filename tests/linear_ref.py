@@ -4,9 +4,10 @@ Exactness: with small-integer operands every product and every partial sum is an
 2^24, which fp32 holds exactly in whatever order and with whatever truncation it is summed, so
 without an activation the stored result is the exact value rounded once.
 
-With an activation, z is exact and act(z) is a few fp32 operations on it: CUDA documents erff
-within 2 ulp, __expf(t) within 2 + 1.173 |t| ulp, __fdividef within 2 ulp.  0.5 z (1 + erf) is then
-within 16 EPS32 (|z| + 1), the argument's roundings amplified by at most |z| f' <= 1 included.
+With an activation, z is exact and act(z) is a few fp32 operations on it: CUDA documents
+__expf(t) within 2 + 1.173 |t| ulp and __fdividef within 2 ulp.  z Phi(z): the formula is within
+0.75e-7 = 1.3 EPS32 of Phi, and its evaluation, q e^(-x^2) / 2 with q <= 1 and x^2 e^(-x^2) <= 0.37, adds
+at most (2 (2 + 1.173 0.37) + 4) / 2 EPS32 by the power and 8 by quotient and polynomial: within 16 EPS32 (|z| + 1).
 z s with s = 1 / (1 + e^-t): e's relative error 2 EPS32 (2 + 1.173 |t|) and the argument's 4 roundings
 (4 |t| EPS32) reach s by the factor s (1 - s), and s (1 - s) |t| < 0.23, s (1 - s) <= 0.25: at most
 (1 + 0.6 + 0.9) EPS32, the quotient adds 4 EPS32 s and the product 1: within 16 EPS32 (|z| + 1).

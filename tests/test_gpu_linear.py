@@ -57,6 +57,7 @@ SHAPES = {
     "tiles_128": (300, 256, 6400, 0, 0, 0, 0, 0),
     "single_split8": (300, 8192, 300, 0, 0, 0, 0, 0),
     "single_no_split": (70, 72, 260, 0, 0, 0, 0, 0),
+    "pairs_long": (2560, 17000, 2050, 0, 0, 0, 0, 0),
     "pairs_one_column_tile": (20000, 64, 130, 0, 0, 0, 0, 0),
 }
 
@@ -112,7 +113,8 @@ def test_gradients_exact(name, dwt, cuda_device):
 
 
 @pytest.mark.parametrize("a", [GELU, TANH, SILU])
-@pytest.mark.parametrize("name", ["one_token_odd", "tokens_33_ragged", "tokens_64_heads", "pairs_ragged"])
+@pytest.mark.parametrize("name", ["one_token_odd", "tokens_33_ragged", "tokens_64_heads", "pairs_ragged", "pairs_odd", "pairs_chunks",
+                                  "single_split8"])
 def test_activations(name, a, cuda_device):
     M, K, N, ih, oh, *_ = SHAPES[name]
     g = _gen(3)
