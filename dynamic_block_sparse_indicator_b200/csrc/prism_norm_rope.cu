@@ -66,6 +66,15 @@ template <> struct Vec8<__nv_bfloat16> {
             f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
         }
     }
+    // the values that lane `from` holds
+    __device__ __forceinline__ Vec8 of(int from) const {
+        Vec8 o;
+        o.r.x = __shfl_sync(0xffffffffu, r.x, from);
+        o.r.y = __shfl_sync(0xffffffffu, r.y, from);
+        o.r.z = __shfl_sync(0xffffffffu, r.z, from);
+        o.r.w = __shfl_sync(0xffffffffu, r.w, from);
+        return o;
+    }
     static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
         __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
                                                        pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
@@ -80,6 +89,18 @@ template <> struct Vec8<float> {
     __device__ __forceinline__ void get(float* f) const {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    __device__ __forceinline__ Vec8 of(int from) const {
+        Vec8 o;
+        o.a.x = __shfl_sync(0xffffffffu, a.x, from);
+        o.a.y = __shfl_sync(0xffffffffu, a.y, from);
+        o.a.z = __shfl_sync(0xffffffffu, a.z, from);
+        o.a.w = __shfl_sync(0xffffffffu, a.w, from);
+        o.b.x = __shfl_sync(0xffffffffu, b.x, from);
+        o.b.y = __shfl_sync(0xffffffffu, b.y, from);
+        o.b.z = __shfl_sync(0xffffffffu, b.z, from);
+        o.b.w = __shfl_sync(0xffffffffu, b.w, from);
+        return o;
     }
     static __device__ __forceinline__ void store(float* p, const float* f) {
         __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
@@ -134,13 +155,18 @@ __device__ __forceinline__ void read_w(const float4* sw, int ch, float* w) {
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
-// A lane's part of the rotation at one token.  Adjacent pairs (2p, 2p + 1) lie in one
-// lane: four (cos, sin).  With halves, channel p of an axis of d channels pairs with
-// p + d / 2, in general in another lane at no alignment (d / 2 may be odd), so the row
-// passes through shared memory and the lane keeps its eight channels' cos, sin (the
-// sign of the channel's own side folded in) and partners.  Channels behind the last
-// axis are not rotated: cos 1, sin 0.
-template <bool HALVES> struct Turn;
+// A lane's part of the rotation at one token, by how the pairs lie.
+//   kAdjacent  (2p, 2p + 1), in one lane: four (cos, sin).
+//   kHalves    channel p of an axis of d channels pairs with p + d / 2, in general in another lane at
+//              no alignment (d / 2 may be odd): the row passes through shared memory and the lane
+//              keeps its eight channels' cos, sin (the sign of the channel's own side folded in)
+//              and the places of their partners.
+//   kLanes     halves of axes whose d / 2 is a multiple of 8: the partners of a lane's channels are
+//              the channels of one other lane, brought by shuffles of the loaded words (40 heads of
+//              92,160 tokens, bf16: forward 5.6 TB/s and backward 5.3, through shared memory 5.3 and 4.4).
+// Channels behind the last axis are not rotated: cos 1, sin 0.
+constexpr int kAdjacent = 0, kHalves = 1, kLanes = 2;
+template <int PAIRS> struct Turn;
 
 __device__ __forceinline__ float2 rope_at(const Rope& r, int pair, int t, int h, int w) {
     const int pt = r.dt >> 1, ph = r.dh >> 1, pw = r.dw >> 1;
@@ -152,14 +178,13 @@ __device__ __forceinline__ float2 rope_at(const Rope& r, int pair, int t, int h,
     return make_float2(1.f, 0.f);
 }
 
-template <> struct Turn<false> {
+template <> struct Turn<kAdjacent> {
     float2 cs[4];
     __device__ __forceinline__ void init(const Rope& r, int ch, int t, int h, int w) {
         #pragma unroll
         for (int i = 0; i < 4; ++i) cs[i] = rope_at(r, (ch >> 1) + i, t, h, w);
     }
     // u -> R u (DIR = 1) or R^T u (DIR = -1)
-    static __device__ __forceinline__ void put(const float*, float*, int) {}
     template <int DIR>
     __device__ __forceinline__ void take(float* u, const float*) const {
         #pragma unroll
@@ -171,7 +196,7 @@ template <> struct Turn<false> {
     }
 };
 
-template <> struct Turn<true> {
+template <> struct Turn<kHalves> {
     float c[8], s[8];
     int at[8];               // the partners' places in the row's shared-memory copy
     // one pad word per 8 channels: the lanes of a row write and read at an odd stride
@@ -210,12 +235,42 @@ template <> struct Turn<true> {
     }
 };
 
-// The rotation with a tensor's weights in it, x -> R (w x) (`w` laid out by Turn<true>::place).
-template <bool HALVES> struct Fold;
-template <> struct Fold<false> {
+template <> struct Turn<kLanes> {
+    float c[8], s[8];
+    int partner;             // the partners' first channel
+    __device__ __forceinline__ void init(const Rope& r, int ch, int t, int h, int w) {
+        int base = 0, d = r.dt;
+        if (ch >= r.dt) { base = r.dt; d = r.dh; }
+        if (ch >= r.dt + r.dh) { base = r.dt + r.dh; d = r.dw; }
+        const int l = ch - base, half = d >> 1;
+        const bool turns = l < d, lo = l < half;
+        partner = !turns ? ch : lo ? ch + half : ch - half;
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 v = turns ? rope_at(r, (base >> 1) + (lo ? l : l - half) + i, t, h, w) : make_float2(1.f, 0.f);
+            c[i] = v.x;
+            s[i] = lo ? -v.y : v.y;
+        }
+    }
+    __device__ __forceinline__ int from(int lane, int lanes) const { return (lane & ~(lanes - 1)) | (partner >> 3); }
+    template <int DIR>
+    __device__ __forceinline__ void take(float* u, const float* p) const {
+        #pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            float p0, p1;
+            fmul2(p0, p1, p[i], p[i + 1], DIR * s[i], DIR * s[i + 1]);
+            ffma2(u[i], u[i + 1], u[i], u[i + 1], c[i], c[i + 1], p0, p1);
+        }
+    }
+};
+
+// The rotation with a tensor's weights in it, x -> R (w x) (`w` laid out by place()).
+__device__ __forceinline__ int place(int ch) { return Turn<kHalves>::place(ch); }
+template <int PAIRS> struct Fold;
+template <> struct Fold<kAdjacent> {
     float a0[4], b0[4], a1[4], b1[4];        // y_a = x_a a0 + x_b b0, y_b = x_a a1 + x_b b1
     __device__ __forceinline__ void init(const Rope& r, const float* w, int ch, int t, int h, int g) {
-        const float* own = w + Turn<true>::place(ch);
+        const float* own = w + Turn<kHalves>::place(ch);
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 cs = r.tab ? rope_at(r, (ch >> 1) + i, t, h, g) : make_float2(1.f, 0.f);
@@ -233,25 +288,37 @@ template <> struct Fold<false> {
         }
     }
 };
-template <> struct Fold<true> {
-    Turn<true> turn;
+template <> struct Fold<kHalves> {
+    Turn<kHalves> turn;
     __device__ __forceinline__ void init(const Rope& r, const float* w, int ch, int t, int h, int g) {
         turn.init(r, ch, t, h, g);
         #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            turn.c[e] *= w[Turn<true>::place(ch) + e];
+            turn.c[e] *= w[Turn<kHalves>::place(ch) + e];
             turn.s[e] *= w[turn.at[e]];
         }
     }
     __device__ __forceinline__ void apply(float* x, const float* row) const { turn.take<1>(x, row); }
 };
+template <> struct Fold<kLanes> {
+    Turn<kLanes> turn;
+    __device__ __forceinline__ void init(const Rope& r, const float* w, int ch, int t, int h, int g) {
+        turn.init(r, ch, t, h, g);
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            turn.c[e] *= w[place(ch) + e];
+            turn.s[e] *= w[place(turn.partner) + e];
+        }
+    }
+    __device__ __forceinline__ void apply(float* x, const float* p) const { turn.take<1>(x, p); }
+};
 
-// Rows of a group, and shared memory for their exchange (HALVES only).
-template <typename T, int D, bool HALVES, int U>
+// Rows of a group, and shared memory for their exchange (kHalves only).
+template <typename T, int D, int PAIRS, int U>
 struct Group {
     static constexpr int kRows = kThreads / (D / 8);      // rows of one head in a block
     static constexpr int kPitch = D + D / 8;
-    static constexpr int kFloats = HALVES ? U * kRows * kPitch : 1;
+    static constexpr int kFloats = PAIRS == kHalves ? U * kRows * kPitch : 1;
 };
 
 __device__ __forceinline__ void grid_at(const Rope& r, int64_t n, int& t, int& h, int& w) {
@@ -284,10 +351,11 @@ __device__ __forceinline__ void scale8(float* x, float r) {
 // halves 5.3: there shared memory is 82% busy, eight words written and eight read per lane and row
 // (unfolded, every row summed by itself: 4.3).  At 5 heads, 1,013,760 tokens, 5.1: a token's factors
 // and addresses serve ten rows only.
-template <typename TI, typename TO, int D, bool HALVES>
-__global__ void __launch_bounds__(kThreads, HALVES ? 3 : 4) k_norm_rope(const Args a) {
+template <typename TI, typename TO, int D, int PAIRS>
+__global__ void __launch_bounds__(kThreads, PAIRS == kAdjacent ? 4 : 3) k_norm_rope(const Args a) {
     constexpr int U = sizeof(TI) == 2 ? 4 : 2;
-    using G = Group<TI, D, HALVES, U>;
+    constexpr bool HALVES = PAIRS == kHalves;
+    using G = Group<TI, D, PAIRS, U>;
     constexpr int LANES = D / 8, RPB = G::kRows;
     __shared__ float sx[G::kFloats];
     __shared__ float sw[2][D + D / 8];
@@ -295,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, HALVES ? 3 : 4) k_norm_rope(const Ar
     float* row = HALVES ? sx + sub * G::kPitch : sx;
     const int h0 = blockIdx.y * a.hpc, h1 = min(h0 + a.hpc, a.heads);
     for (int i = threadIdx.x; i < a.tensors * D; i += kThreads)
-        sw[i / D][Turn<true>::place(i % D)] = weight_at(a.w[i / D], a.w_f32, i % D);
+        sw[i / D][Turn<kHalves>::place(i % D)] = weight_at(a.w[i / D], a.w_f32, i % D);
     __syncthreads();
     for (int64_t n0 = (int64_t)blockIdx.x * RPB; n0 < a.N; n0 += (int64_t)gridDim.x * RPB) {
         const int64_t n = n0 + sub;
@@ -303,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, HALVES ? 3 : 4) k_norm_rope(const Ar
         int gt = 0, gh = 0, gw = 0;
         if (a.rope.tab) grid_at(a.rope, ok ? n : 0, gt, gh, gw);
         for (int z = 0; z < a.tensors; ++z) {
-            Fold<HALVES> fold;
+            Fold<PAIRS> fold;
             fold.init(a.rope, sw[z], ch, gt, gh, gw);
             const TI* src = static_cast<const TI*>(a.in[z].p) + n * a.in[z].ts + h0 * a.in[z].hs + ch;
             TO* dst = static_cast<TO*>(a.out[z].p) + n * a.out[z].ts + h0 * a.out[z].hs + ch;
@@ -320,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, HALVES ? 3 : 4) k_norm_rope(const Ar
                 for (int i = 0; i < U; ++i) {
                     float x[8];
                     v[i].get(x);
-                    if (HALVES) Turn<true>::put(x, row + i * RPB * G::kPitch, ch);
+                    if (HALVES) Turn<kHalves>::put(x, row + i * RPB * G::kPitch, ch);
                     r[i] = squares(x);
                 }
                 if (HALVES) __syncwarp();
@@ -332,7 +400,13 @@ __global__ void __launch_bounds__(kThreads, HALVES ? 3 : 4) k_norm_rope(const Ar
                     if (h + i >= h1) break;          // the same for the whole block
                     float x[8];
                     v[i].get(x);
-                    fold.apply(x, row + i * RPB * G::kPitch);
+                    if constexpr (PAIRS == kLanes) {
+                        float p[8];
+                        v[i].of(fold.turn.from(lane, LANES)).get(p);
+                        fold.apply(x, p);
+                    } else {
+                        fold.apply(x, row + i * RPB * G::kPitch);
+                    }
                     scale8(x, r[i]);
                     if (ok) Vec8<TO>::store(dst + i * a.out[z].hs, x);
                 }
@@ -345,10 +419,11 @@ __global__ void __launch_bounds__(kThreads, HALVES ? 3 : 4) k_norm_rope(const Ar
 // then holds one weight's sums).  A block sums its rows' part of dw in registers (in the
 // order of its loop), then over its rows through shared memory, and writes one row of
 // partial sums: no atomics, the same bits every time.
-template <typename TI, typename TG, int D, bool HALVES>
+template <typename TI, typename TG, int D, int PAIRS>
 __global__ void __launch_bounds__(kThreads, 2) k_norm_rope_bwd(const Args a) {
     constexpr int U = 4;
-    using G = Group<TG, D, HALVES, U>;
+    constexpr bool HALVES = PAIRS == kHalves, KEEP = PAIRS != kAdjacent;
+    using G = Group<TG, D, PAIRS, U>;
     constexpr int LANES = D / 8, RPB = G::kRows;
     constexpr int kSum = RPB * D;
     __shared__ float sx[kSum > G::kFloats ? kSum : G::kFloats];
@@ -364,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_rope_bwd(const Args a) {
     for (int64_t n0 = (int64_t)blockIdx.x * RPB; n0 < a.N; n0 += (int64_t)gridDim.x * RPB) {
         const int64_t n = n0 + sub;
         const bool ok = n < a.N;
-        Turn<HALVES> turn;
+        Turn<PAIRS> turn;
         if (a.rope.tab) {
             int t, h, w;
             grid_at(a.rope, ok ? n : 0, t, h, w);
@@ -391,23 +466,29 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_rope_bwd(const Args a) {
                 for (int i = 0; i < U; ++i) {
                     float g[8];
                     q[i].get(g);
-                    turn.put(g, row + i * RPB * G::kPitch, ch);
+                    Turn<kHalves>::put(g, row + i * RPB * G::kPitch, ch);
                 }
                 __syncwarp();
             }
             // (with halves the rotated rows stay in registers: reading the exchange twice cost 13% of the
             // bandwidth; adjacent pairs are rotated again, from fewer registers)
-            float w[8], r[U], k[U], kept[HALVES ? U : 1][8];
+            float w[8], r[U], k[U], kept[KEEP ? U : 1][8];
             read_w(sw[0], ch, w);
             #pragma unroll
             for (int i = 0; i < U; ++i) {
                 float x[8], g[8], d0 = 0.f, d1 = 0.f;
                 v[i].get(x);
                 q[i].get(g);
-                if (a.rope.tab) turn.template take<-1>(g, row + i * RPB * G::kPitch);
-                if (HALVES) {
+                if constexpr (PAIRS == kLanes) {
+                    float p[8];
+                    q[i].of(turn.from(lane, LANES)).get(p);
+                    turn.template take<-1>(g, p);
+                } else {
+                    if (a.rope.tab) turn.template take<-1>(g, row + i * RPB * G::kPitch);
+                }
+                if (KEEP) {
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) kept[HALVES ? i : 0][e] = g[e];
+                    for (int e = 0; e < 8; ++e) kept[KEEP ? i : 0][e] = g[e];
                 }
                 r[i] = squares(x);
                 #pragma unroll
@@ -432,9 +513,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_rope_bwd(const Args a) {
                 if (h + i >= h1) break;              // the same for the whole block
                 float x[8], g[8];
                 v[i].get(x);
-                if (HALVES) {
+                if constexpr (KEEP) {
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) g[e] = kept[HALVES ? i : 0][e];
+                    for (int e = 0; e < 8; ++e) g[e] = kept[i][e];
                 } else {
                     q[i].get(g);
                     if (a.rope.tab) turn.template take<-1>(g, nullptr);
@@ -613,32 +694,33 @@ static Rope rope_of(const prism_norm_rope_params* p, const float* table) {
     return r;
 }
 
-template <typename TI, typename TO, bool BWD>
-static void launch(const Args& a, const Grid& g, int D, bool halves, cudaStream_t s) {
+template <typename TI, typename TO, bool BWD, int D>
+static void launch(const Args& a, const Grid& g, int pairs, cudaStream_t s) {
     const dim3 grid(g.x, g.y, g.z);
     if constexpr (BWD) {
-        if (D == 128) halves ? k_norm_rope_bwd<TI, TO, 128, true><<<grid, kThreads, 0, s>>>(a)
-                             : k_norm_rope_bwd<TI, TO, 128, false><<<grid, kThreads, 0, s>>>(a);
-        else halves ? k_norm_rope_bwd<TI, TO, 64, true><<<grid, kThreads, 0, s>>>(a)
-                    : k_norm_rope_bwd<TI, TO, 64, false><<<grid, kThreads, 0, s>>>(a);
+        pairs == kAdjacent ? k_norm_rope_bwd<TI, TO, D, kAdjacent><<<grid, kThreads, 0, s>>>(a)
+        : pairs == kLanes  ? k_norm_rope_bwd<TI, TO, D, kLanes><<<grid, kThreads, 0, s>>>(a)
+                           : k_norm_rope_bwd<TI, TO, D, kHalves><<<grid, kThreads, 0, s>>>(a);
     } else {
-        if (D == 128) halves ? k_norm_rope<TI, TO, 128, true><<<grid, kThreads, 0, s>>>(a)
-                             : k_norm_rope<TI, TO, 128, false><<<grid, kThreads, 0, s>>>(a);
-        else halves ? k_norm_rope<TI, TO, 64, true><<<grid, kThreads, 0, s>>>(a)
-                    : k_norm_rope<TI, TO, 64, false><<<grid, kThreads, 0, s>>>(a);
+        pairs == kAdjacent ? k_norm_rope<TI, TO, D, kAdjacent><<<grid, kThreads, 0, s>>>(a)
+        : pairs == kLanes  ? k_norm_rope<TI, TO, D, kLanes><<<grid, kThreads, 0, s>>>(a)
+                           : k_norm_rope<TI, TO, D, kHalves><<<grid, kThreads, 0, s>>>(a);
     }
 }
 
+template <bool BWD, int D>
+static void by_type(const prism_norm_rope_params* p, const Args& a, const Grid& g, int pairs, cudaStream_t s) {
+    using bf = __nv_bfloat16;
+    const bool in32 = p->dtype == PRISM_F32, out32 = p->out_dtype == PRISM_F32;
+    if (in32) out32 ? launch<float, float, BWD, D>(a, g, pairs, s) : launch<float, bf, BWD, D>(a, g, pairs, s);
+    else out32 ? launch<bf, float, BWD, D>(a, g, pairs, s) : launch<bf, bf, BWD, D>(a, g, pairs, s);
+}
 template <bool BWD>
 static int dispatch(const prism_norm_rope_params* p, const Args& a, const Grid& g, cudaStream_t s) {
-    using bf = __nv_bfloat16;
-    const bool halves = a.rope.tab && p->pairing == PRISM_PAIR_HALVES;
-    if (p->dtype == PRISM_BF16)
-        p->out_dtype == PRISM_BF16 ? launch<bf, bf, BWD>(a, g, p->head_dim, halves, s)
-                                   : launch<bf, float, BWD>(a, g, p->head_dim, halves, s);
-    else
-        p->out_dtype == PRISM_BF16 ? launch<float, bf, BWD>(a, g, p->head_dim, halves, s)
-                                   : launch<float, float, BWD>(a, g, p->head_dim, halves, s);
+    int pairs = kAdjacent;
+    if (a.rope.tab && p->pairing == PRISM_PAIR_HALVES)
+        pairs = (p->dim_t | p->dim_h | p->dim_w) % 16 == 0 ? kLanes : kHalves;
+    p->head_dim == 128 ? by_type<BWD, 128>(p, a, g, pairs, s) : by_type<BWD, 64>(p, a, g, pairs, s);
     return cudaGetLastError() == cudaSuccess ? PRISM_OK : PRISM_ERR_CUDA;
 }
 

@@ -24,6 +24,10 @@ CASES = {
     "no_time_axis": ((1, 16, 24), 4, 64, F32, F32, F32, "padded", 0, (0, 32, 32)),
     "fp32_to_bf16": ((4, 5, 6), 3, 128, F32, BF, F32, "fused", 0, (32, 48, 48)),
     "fp32_halves": ((4, 5, 6), 3, 128, F32, F32, None, "heads", 1, (32, 48, 48)),
+    "lanes_1d": ((37, 1, 1), 5, 128, BF, BF, F32, "fused", 1, (128, 0, 0)),
+    "lanes_grid": ((3, 7, 11), 5, 128, BF, BF, BF, "heads", 1, (32, 48, 48)),
+    "lanes_d64_fp32": ((5, 3, 7), 3, 64, F32, F32, F32, "padded", 1, (32, 16, 0)),
+    "lanes_no_time_axis": ((1, 6, 9), 2, 128, BF, F32, F32, "heads", 1, (0, 64, 48)),
     "two_channels": ((9, 1, 2), 2, 64, F32, F32, BF, "heads", 1, (2, 0, 0)),
     "nothing_rotated": ((6, 5, 4), 2, 64, BF, BF, F32, "heads", 0, (0, 0, 0)),
     "far_positions": ((40000, 1, 1), 1, 64, F32, F32, F32, "heads", 0, (64, 0, 0)),
@@ -90,7 +94,7 @@ def test_gradients(name, cuda_device):
             _within(gw, dw, (48 + walked * x.shape[0]) * ref.EPS32 * mag, n + " weight")
 
 
-@pytest.mark.parametrize("name", ["grid_5x7x9", "fp32_halves", "grid_3x11x13_partial"])
+@pytest.mark.parametrize("name", ["grid_5x7x9", "fp32_halves", "grid_3x11x13_partial", "lanes_grid"])
 def test_gradients_against_differences(name, cuda_device):
     """<dx, d> and <dw, e> against central differences of the 64-bit forward."""
     q, k, ws, dy, rope, ang, ab, ot = _case(name, 2)
