@@ -421,7 +421,10 @@ __global__ void __launch_bounds__(kThreads, PAIRS == kAdjacent ? 4 : 3) k_norm_r
 // partial sums: no atomics, the same bits every time.
 template <typename TI, typename TG, int D, int PAIRS>
 __global__ void __launch_bounds__(kThreads, 2) k_norm_rope_bwd(const Args a) {
-    constexpr int U = 4;
+    // rows at a time: four, but two where four rows' fp32 gradients and their exchange do not fit the
+    // registers (40 heads of 92,160 tokens, halves: fp32 5.0 TB/s with two and 4.0 with four, bf16 4.0
+    // and 4.6; adjacent 5.6 and 6.6, 3.6 and 5.4)
+    constexpr int U = PAIRS == kHalves && sizeof(TG) == 4 ? 2 : 4;
     constexpr bool HALVES = PAIRS == kHalves, KEEP = PAIRS != kAdjacent;
     using G = Group<TG, D, PAIRS, U>;
     constexpr int LANES = D / 8, RPB = G::kRows;
