@@ -533,51 +533,50 @@ def status_read(status, stream=None):
 
 # ---- the layer's operators around the attention -----------------------------------------
 
+_codes: dict = {}
+
+
 def _code(dtype, what):
     """PRISM_BF16 / PRISM_F32 of a torch dtype."""
-    import torch
-    if dtype == torch.bfloat16:
-        return PRISM_BF16
-    if dtype == torch.float32:
-        return PRISM_F32
-    raise ValueError(f"{what} must be bfloat16 or float32, got {dtype}")
+    if not _codes:
+        import torch
+        _codes.update({torch.bfloat16: PRISM_BF16, torch.float32: PRISM_F32})
+    code = _codes.get(dtype)
+    if code is None:
+        raise ValueError(f"{what} must be bfloat16 or float32, got {dtype}")
+    return code
 
 
 class _Launch:
-    """The device and stream of a call.  Makes the tensors' device current.  Where the call runs
-    on another stream than torch's current one, what it allocates comes from that stream (memory
-    that the current stream may still be using is not written) and counts as used by both, and
-    the tensors given count as used there: none is handed out again before that work is done.
-    Ordering the two streams is the caller's, as everywhere."""
+    """The device and stream of a call.  The library is called with the tensors' device current.
+    Where the call runs on another stream than torch's current one, what it allocates comes from
+    that stream (memory that the current stream may still be using is not written) and counts as
+    used by both, and the tensors given count as used there: none is handed out again before that
+    work is done.  Ordering the two streams is the caller's, as everywhere."""
+    __slots__ = ("first", "tensors", "device", "s", "cur", "other", "stream", "guard")
 
     def __init__(self, tensors, stream):
         import torch
-        first = tensors[0]
-        dev = first.device
+        first = self.first = tensors[0]
+        d = first.get_device()
         for t in tensors:
-            if t is not None and (t.device != dev or not t.is_cuda):
+            if t is not None and (t.get_device() != d or d < 0):
                 raise ValueError("the tensors must be on one CUDA device")
-        self.first, self.tensors = first, tensors
-        self.guard = torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else None
-        cur = self.cur = torch.cuda.current_stream(dev)
+        self.tensors = tensors
+        self.guard = None
+        if torch.cuda.current_device() != d:
+            self.guard = torch.cuda.device(d)
         self.other = False
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-            self.other = stream.cuda_stream != cur.cuda_stream
-            cur = stream
-        self.s = cur
-        self.stream = cur.cuda_stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+        if stream is None:
+            self.s = self.cur = None
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            self.stream = raw(d) if raw is not None else torch.cuda.current_stream(d).cuda_stream
+        else:
+            if stream.device.index != d:
+                raise ValueError(f"the stream is on {stream.device}, the tensors are on {first.device}")
+            self.s, self.cur = stream, torch.cuda.current_stream(d)
+            self.stream = stream.cuda_stream
+            self.other = self.stream != self.cur.cuda_stream
 
     def empty(self, shape, dtype):
         """Memory for the call."""
@@ -592,14 +591,20 @@ class _Launch:
     def zero_status(self):
         """A device status block for the call, cleared on its stream."""
         import torch
+        if not self.other:
+            return self.first.new_zeros(4, dtype=torch.int32)
         with torch.cuda.stream(self.s):
             t = self.first.new_zeros(4, dtype=torch.int32)
-        if self.other:
-            t.record_stream(self.cur)
+        t.record_stream(self.cur)
         return t
 
-    def check(self, status, what):
-        """Raises on a status; a call on another stream marks the given tensors as used there."""
+    def call(self, what, fn, *args):
+        """fn(*args, stream) with the device current; raises on a status."""
+        if self.guard is None:
+            status = fn(*args, self.stream)
+        else:
+            with self.guard:
+                status = fn(*args, self.stream)
         if status:
             raise PrismError(status, what)
         if self.other:
@@ -641,9 +646,8 @@ def make_rope(T, H, W, dims, theta=10000.0, pairing=PRISM_PAIR_ADJACENT, first_f
     rope = Rope(table, int(T), int(H), int(W), dims, int(pairing))
     D = 64 if sum(dims) <= 64 else 128
     p = _norm_rope_params(T * H * W, 1, D, PRISM_BF16, PRISM_BF16, PRISM_F32, rope, 1.0)
-    with _Launch([table], stream) as go:
-        go.check(load().prism_rope_table(C.byref(p), float(theta), int(first_frame), table.data_ptr(), go.stream),
-                 "prism_rope_table")
+    _Launch([table], stream).call("prism_rope_table", load().prism_rope_table, C.byref(p), float(theta), int(first_frame),
+                                  table.data_ptr())
     return rope
 
 
@@ -660,7 +664,7 @@ def _rows(t, what):
 def _weights(ws, D, what):
     ws = [w for w in ws if w is not None]
     for w in ws:
-        if tuple(w.shape) != (D,) or not w.is_contiguous() or w.dtype != ws[0].dtype:
+        if w.shape != (D,) or not w.is_contiguous() or w.dtype != ws[0].dtype:
             raise ValueError(f"{what} must be contiguous vectors of the {D} channels, of one type")
     return _code(ws[0].dtype, what) if ws else PRISM_F32
 
@@ -704,14 +708,14 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, rope=None, eps=1e-6, q_out=None, k
     if wk is not None and k is None:
         raise ValueError("wk without k")
     dt, odt, wdt = _code(q.dtype, "q"), _code(out_dtype, "the result"), _weights((wq, wk), D, "wq and wk")
-    with _Launch([q, k, wq, wk, q_out, k_out, rope.table if rope is not None else None], stream) as go:
-        if q_out is None:
-            q_out = go.empty(q.shape, out_dtype)
-            k_out = go.empty(k.shape, out_dtype) if k is not None else None
-        p = _norm_rope_params(N, heads, D, dt, odt, wdt, rope, eps)
-        go.check(load().prism_qk_norm_rope(C.byref(p), _rows(q, "q"), _rows(k, "k"), _at(wq), _at(wk),
-                                           _at(rope.table) if rope is not None else None, _rows(q_out, "q_out"),
-                                           _rows(k_out, "k_out"), go.stream), "prism_qk_norm_rope")
+    table = None if rope is None else rope.table
+    go = _Launch((q, k, wq, wk, q_out, k_out, table), stream)
+    if q_out is None:
+        q_out = go.empty(q.shape, out_dtype)
+        k_out = go.empty(k.shape, out_dtype) if k is not None else None
+    p = _norm_rope_params(N, heads, D, dt, odt, wdt, rope, eps)
+    go.call("prism_qk_norm_rope", load().prism_qk_norm_rope, C.byref(p), _rows(q, "q"), _rows(k, "k"), _at(wq), _at(wk),
+            _at(table), _rows(q_out, "q_out"), _rows(k_out, "k_out"))
     return q_out, k_out
 
 
@@ -733,29 +737,27 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k=None, wq=None, wk=None, rope=None, eps
     if wk is not None and k is None:
         raise ValueError("wk without k")
     dt, gdt, wdt = _code(q.dtype, "q"), _code(dq_out.dtype, "dq_out"), _weights((wq, wk), D, "wq and wk")
-    with _Launch([q, k, dq_out, dk_out, wq, wk, dq, dk, workspace, rope.table if rope is not None else None],
-                 stream) as go:
-        def like(x):
-            """Dense, in the order of x's strides: token-major rows stay token-major."""
-            if x is None:
-                return None
-            if x.stride(1) > x.stride(0):
-                return go.empty((N, heads, D), x.dtype).transpose(0, 1)
-            return go.empty((heads, N, D), x.dtype)
+    table = None if rope is None else rope.table
+    go = _Launch((q, k, dq_out, dk_out, wq, wk, dq, dk, workspace, table), stream)
 
-        if dq is None:
-            dq, dk = like(q), like(k)
-        dwq = go.empty((D,), torch.float32) if want_dw and wq is not None else None
-        dwk = go.empty((D,), torch.float32) if want_dw and wk is not None else None
-        p = _norm_rope_params(N, heads, D, dt, gdt, wdt, rope, eps)
-        lib = load()
-        if workspace is None and (dwq is not None or dwk is not None):
-            workspace = go.empty((max(int(lib.prism_qk_norm_rope_bwd_workspace_bytes(C.byref(p))), 16),), torch.uint8)
-        go.check(lib.prism_qk_norm_rope_bwd(C.byref(p), _rows(dq_out, "dq_out"), _rows(dk_out, "dk_out"), _rows(q, "q"),
-                                            _rows(k, "k"), _at(wq), _at(wk),
-                                            _at(rope.table) if rope is not None else None, _rows(dq, "dq"),
-                                            _rows(dk, "dk"), _at(dwq), _at(dwk), _at(workspace), _size(workspace),
-                                            go.stream), "prism_qk_norm_rope_bwd")
+    def like(x):
+        """Dense, in the order of x's strides: token-major rows stay token-major."""
+        if x.stride(1) > x.stride(0):
+            return go.empty((N, heads, D), x.dtype).transpose(0, 1)
+        return go.empty((heads, N, D), x.dtype)
+
+    if dq is None:
+        dq = like(q)
+        dk = like(k) if k is not None else None
+    dwq = go.empty((D,), torch.float32) if want_dw and wq is not None else None
+    dwk = go.empty((D,), torch.float32) if want_dw and wk is not None else None
+    p = _norm_rope_params(N, heads, D, dt, gdt, wdt, rope, eps)
+    lib = load()
+    if workspace is None and (dwq is not None or dwk is not None):
+        workspace = go.empty((max(int(lib.prism_qk_norm_rope_bwd_workspace_bytes(C.byref(p))), 16),), torch.uint8)
+    go.call("prism_qk_norm_rope_bwd", lib.prism_qk_norm_rope_bwd, C.byref(p), _rows(dq_out, "dq_out"),
+            _rows(dk_out, "dk_out"), _rows(q, "q"), _rows(k, "k"), _at(wq), _at(wk), _at(table), _rows(dq, "dq"),
+            _rows(dk, "dk"), _at(dwq), _at(dwk), _at(workspace), _size(workspace))
     return dq, dk, dwq, dwk
 
 
@@ -780,6 +782,13 @@ def _features(t, what, dtype=None):
 
 def _shape_like(M, F, heads):
     return (heads, M, F // heads) if heads else (M, F)
+
+
+def _in_layout(t, what, shape, dtype):
+    """The row stride of a tensor that must have this shape and type."""
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected {shape}, got {tuple(t.shape)}")
+    return _features(t, what, dtype)[3]
 
 
 def _size(t):
@@ -813,29 +822,27 @@ def linear(x, W, bias=None, residual=None, activation=PRISM_ACT_NONE, y=None, ou
     if out_heads and (out_heads < 0 or N % out_heads or N // out_heads not in (64, 128)):
         raise ValueError(f"{N} features are not {out_heads} heads of 64 or 128 channels")
     want = _shape_like(M, N, out_heads)
-    strides = [N, N]
-    for i, (t, what) in enumerate(((y, "y"), (residual, "residual"))):
-        if t is not None:
-            if tuple(t.shape) != want:
-                raise ValueError(f"{what}: expected {want}, got {tuple(t.shape)}")
-            strides[i] = _features(t, what, out_dtype)[3]
-    if pre is not None and (tuple(pre.shape) != want or pre.dtype != torch.bfloat16 or not pre.is_contiguous()):
+    y_stride = N if y is None else _in_layout(y, "y", want, out_dtype)
+    r_stride = N if residual is None else _in_layout(residual, "residual", want, out_dtype)
+    if pre is not None and (pre.shape != want or pre.dtype != torch.bfloat16 or not pre.is_contiguous()):
         raise ValueError(f"pre must be a contiguous bf16 {want}")
-    if bias is not None and (tuple(bias.shape) != (N,) or not bias.is_contiguous()):
+    if bias is not None and (bias.shape != (N,) or not bias.is_contiguous()):
         raise ValueError(f"bias must be [{N}]")
     p = PrismLinearParams(M, K, N, in_heads, out_heads, int(activation), _code(out_dtype, "y"),
-                          PRISM_F32 if bias is None else _code(bias.dtype, "bias"), PRISM_F32, xs, ws_, strides[0], strides[1])
+                          PRISM_F32 if bias is None else _code(bias.dtype, "bias"), PRISM_F32, xs, ws_, y_stride, r_stride)
     _check_status(status)
     lib = load()
-    with _Launch([x, W, bias, residual, y, pre, workspace, status], stream) as go:
-        y = go.empty(want, out_dtype) if y is None else y
-        if want_pre and pre is None:
-            pre = go.empty(want, torch.bfloat16)
-        if workspace is None and (xs % 8 or ws_ % 8):
-            workspace = go.empty((max(int(lib.prism_linear_workspace_bytes(C.byref(p))), 16),), torch.uint8)
-        status = go.zero_status() if status is None else status
-        go.check(lib.prism_linear(C.byref(p), x.data_ptr(), W.data_ptr(), _at(bias), _at(residual), y.data_ptr(), _at(pre),
-                                  _at(workspace), _size(workspace), status.data_ptr(), go.stream), "prism_linear")
+    go = _Launch((x, W, bias, residual, y, pre, workspace, status), stream)
+    if y is None:
+        y = go.empty(want, out_dtype)
+    if want_pre and pre is None:
+        pre = go.empty(want, torch.bfloat16)
+    if workspace is None and (xs % 8 or ws_ % 8):
+        workspace = go.empty((max(int(lib.prism_linear_workspace_bytes(C.byref(p))), 16),), torch.uint8)
+    if status is None:
+        status = go.zero_status()
+    go.call("prism_linear", lib.prism_linear, C.byref(p), x.data_ptr(), W.data_ptr(), _at(bias), _at(residual),
+            y.data_ptr(), _at(pre), _at(workspace), _size(workspace), status.data_ptr())
     return y, pre, status
 
 
@@ -854,7 +861,7 @@ def linear_bwd(dy, x, W, pre=None, activation=PRISM_ACT_NONE, dx=None, dW=None, 
         raise ValueError(f"dy has {Mo} rows of {No} features, expected {M} of {N}")
     want = _shape_like(M, N, out_heads)
     if activation != PRISM_ACT_NONE:
-        if pre is None or tuple(pre.shape) != want or pre.dtype != torch.bfloat16 or not pre.is_contiguous():
+        if pre is None or pre.shape != want or pre.dtype != torch.bfloat16 or not pre.is_contiguous():
             raise ValueError(f"the activation's gradient needs pre, a contiguous bf16 {want}")
     else:
         pre = None
@@ -867,13 +874,17 @@ def linear_bwd(dy, x, W, pre=None, activation=PRISM_ACT_NONE, dx=None, dW=None, 
                           _code(dw_dtype, "dW"), xs, ws_, ys, N)
     _check_status(status)
     lib = load()
-    with _Launch([dy, x, W, pre, dx, dW, db, workspace, status], stream) as go:
-        dx = go.empty(x.shape, torch.bfloat16) if dx is None and want_dx else dx
-        dW = go.empty((N, K), dw_dtype) if dW is None and want_dw else dW
-        db = go.empty((N,), torch.float32) if db is None and want_db else db
-        if workspace is None:
-            workspace = go.empty((max(int(lib.prism_linear_bwd_workspace_bytes(C.byref(p))), 16),), torch.uint8)
-        status = go.zero_status() if status is None else status
-        go.check(lib.prism_linear_bwd(C.byref(p), dy.data_ptr(), x.data_ptr(), W.data_ptr(), _at(pre), _at(dx), _at(dW), _at(db),
-                                      _at(workspace), _size(workspace), status.data_ptr(), go.stream), "prism_linear_bwd")
+    go = _Launch((dy, x, W, pre, dx, dW, db, workspace, status), stream)
+    if dx is None and want_dx:
+        dx = go.empty(x.shape, torch.bfloat16)
+    if dW is None and want_dw:
+        dW = go.empty((N, K), dw_dtype)
+    if db is None and want_db:
+        db = go.empty((N,), torch.float32)
+    if workspace is None:
+        workspace = go.empty((max(int(lib.prism_linear_bwd_workspace_bytes(C.byref(p))), 16),), torch.uint8)
+    if status is None:
+        status = go.zero_status()
+    go.call("prism_linear_bwd", lib.prism_linear_bwd, C.byref(p), dy.data_ptr(), x.data_ptr(), W.data_ptr(), _at(pre),
+            _at(dx), _at(dW), _at(db), _at(workspace), _size(workspace), status.data_ptr())
     return dx, dW, db, status
