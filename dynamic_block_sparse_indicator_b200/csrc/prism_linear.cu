@@ -251,6 +251,25 @@ __device__ __forceinline__ float act_grad(float z, int act) {
     }
 }
 
+template <int NC>
+__device__ __forceinline__ void activate(float* z, int act) {
+    switch (act) {
+        case PRISM_ACT_GELU:
+            #pragma unroll
+            for (int i = 0; i < NC; ++i) z[i] = act_of(z[i], PRISM_ACT_GELU);
+            break;
+        case PRISM_ACT_GELU_TANH:
+            #pragma unroll
+            for (int i = 0; i < NC; ++i) z[i] = act_of(z[i], PRISM_ACT_GELU_TANH);
+            break;
+        case PRISM_ACT_SILU:
+            #pragma unroll
+            for (int i = 0; i < NC; ++i) z[i] = act_of(z[i], PRISM_ACT_SILU);
+            break;
+        default: break;
+    }
+}
+
 // One lane's column c of C: where its elements lie.
 struct Lane {
     char* y;
@@ -284,31 +303,41 @@ __device__ __forceinline__ Lane lane_of(const Args& a, int c) {
 template <int NC>
 __device__ __forceinline__ void emit(const Args& a, const Lane& l, int64_t r0, int n, const float* v) {
     if (!l.on) return;
-    float res[NC];
+    float res[NC], z[NC];
     if (l.res) {
-        #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            res[j] = 0.f;
-            if (j < n) {
-                const char* p = l.res + (r0 + j) * l.rs;
-                res[j] = a.res.f32 ? *reinterpret_cast<const float*>(p)
-                                   : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
-            }
+        const char* p = l.res + r0 * l.rs;
+        if (a.res.f32) {
+            #pragma unroll
+            for (int j = 0; j < NC; ++j, p += l.rs) res[j] = j < n ? *reinterpret_cast<const float*>(p) : 0.f;
+        } else {
+            #pragma unroll
+            for (int j = 0; j < NC; ++j, p += l.rs)
+                res[j] = j < n ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p)) : 0.f;
         }
     }
     #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        if (j < n) {
-            const int64_t r = r0 + j;
-            float z = v[j] + l.bias;
-            // the kept z has the operands' 16 bits: the backward forms dz from it for 16-bit products
-            if (l.pre) *reinterpret_cast<__nv_bfloat16*>(l.pre + r * l.ps) = __float2bfloat16_rn(z);
-            if (a.act != PRISM_ACT_NONE) z = act_of(z, a.act);
-            if (l.res) z += res[j];
-            char* p = l.y + r * l.ys;
-            if (a.y.f32) *reinterpret_cast<float*>(p) = z;
-            else *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(z);
-        }
+    for (int j = 0; j < NC; ++j) z[j] = v[j] + l.bias;
+    if (l.pre) {
+        // the kept z has the operands' 16 bits: the backward forms dz from it for 16-bit products
+        char* p = l.pre + r0 * l.ps;
+        #pragma unroll
+        for (int j = 0; j < NC; ++j, p += l.ps)
+            if (j < n) *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(z[j]);
+    }
+    activate<NC>(z, a.act);
+    if (l.res) {
+        #pragma unroll
+        for (int j = 0; j < NC; ++j) z[j] += res[j];
+    }
+    char* p = l.y + r0 * l.ys;
+    if (a.y.f32) {
+        #pragma unroll
+        for (int j = 0; j < NC; ++j, p += l.ys)
+            if (j < n) *reinterpret_cast<float*>(p) = z[j];
+    } else {
+        #pragma unroll
+        for (int j = 0; j < NC; ++j, p += l.ys)
+            if (j < n) *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(z[j]);
     }
 }
 
@@ -589,21 +618,7 @@ __device__ __forceinline__ void finish(const Args& a, float* z, int64_t r, int c
                 if (i < n) p[i] = __float2bfloat16_rn(z[i]);
         }
     }
-    if (ACT) switch (a.act) {
-        case PRISM_ACT_GELU:
-            #pragma unroll
-            for (int i = 0; i < NC; ++i) z[i] = act_of(z[i], PRISM_ACT_GELU);
-            break;
-        case PRISM_ACT_GELU_TANH:
-            #pragma unroll
-            for (int i = 0; i < NC; ++i) z[i] = act_of(z[i], PRISM_ACT_GELU_TANH);
-            break;
-        case PRISM_ACT_SILU:
-            #pragma unroll
-            for (int i = 0; i < NC; ++i) z[i] = act_of(z[i], PRISM_ACT_SILU);
-            break;
-        default: break;
-    }
+    if (ACT) activate<NC>(z, a.act);
     if (RES && a.res.p && r < a.R) {
         if (a.res.f32) {
             const float* p = static_cast<const float*>(a.res.p) + at(a.res, c) + r * a.res.rs;
@@ -943,13 +958,13 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                     __syncwarp();
                     const Lane l = lane_of(a, c + lane);
                     #pragma unroll 1
-                    for (int j = 0; j < 32; j += 8) {
+                    for (int j = 0; j < 32; j += 16) {
                         const int64_t left = a.R - (r0 + j);
                         if (left <= 0) break;
-                        float x[8];
+                        float x[16];
                         #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = ld_shared_f32(stage + swz128(j + i, lane >> 2) + (lane & 3) * 4);
-                        emit<8>(a, l, r0 + j, left < 8 ? (int)left : 8, x);
+                        for (int i = 0; i < 16; ++i) x[i] = ld_shared_f32(stage + swz128(j + i, lane >> 2) + (lane & 3) * 4);
+                        emit<16>(a, l, r0 + j, left < 16 ? (int)left : 16, x);
                     }
                     __syncwarp();
                 }
