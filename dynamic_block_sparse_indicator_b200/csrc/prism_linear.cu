@@ -654,29 +654,6 @@ __device__ __forceinline__ void finish(const Args& a, float* z, int64_t r, int c
         }
     }
 }
-// Row r's H sums from column c on before the first product: residual and bias.  The residual is
-// read straight into the sums, every load in flight at once.
-template <int H>
-__device__ __forceinline__ void first_sums(const Args& a, float* v, int64_t r, int c) {
-    #pragma unroll
-    for (int e = 0; e < H; ++e) v[e] = 0.f;
-    if (a.res.p && a.res.f32 && a.res.vec && c + H <= a.C && r < a.R) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.res.p) + at(a.res, c) + r * a.res.rs);
-        #pragma unroll
-        for (int e = 0; e < H; e += 4) {
-            const float4 x = p[e / 4];
-            v[e] = x.x; v[e + 1] = x.y; v[e + 2] = x.z; v[e + 3] = x.w;
-        }
-        #pragma unroll
-        for (int e = 0; e < H; e += 8) finish<8, false, false>(a, v + e, r, c + e, 8);
-        return;
-    }
-    #pragma unroll
-    for (int e = 0; e < H; e += 8) {
-        const int n = min(8, a.C - (c + e));
-        if (n > 0) finish<8, false>(a, v + e, r, c + e, n);
-    }
-}
 // The same results stored by the thread itself.
 template <int NC>
 __device__ __forceinline__ void store_row(const Args& a, const float* z, int64_t r, int c, int n) {
@@ -823,17 +800,148 @@ template <int CG, int BN>
 constexpr int tile_smem() { return Cfg<CG, BN>::kRing + Cfg<CG, BN>::kEpi * kStageOut + 1024; }
 constexpr int kPartPitch = 132;            // floats per row of a part (CG 1): rows start 4 banks apart
 
+// A warp's 32 rows of 128 bytes (64 bf16 or 32 fp32 columns from c on) between memory and its
+// stage: eight lanes take a row, so an access touches four lines; a lane reading along its own row
+// touched thirty-two.  Chunks of 16 bytes; one that reaches over C's edge goes element by element.
+__device__ __forceinline__ uint4 ld_chunk(const Out& o, const char* p, int cols) {
+    if (cols >= (o.f32 ? 4 : 8)) return *reinterpret_cast<const uint4*>(p);
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (o.f32) {
+        #pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < cols) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    } else {
+        #pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < cols) w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void rows_in(const Args& a, int64_t r0, int c, int lane, uint4* x) {
+    const Out& o = a.res;
+    const int e = o.f32 ? 4 : 2, k = lane & 7, per = 16 / e;
+    const char* p = static_cast<const char*>(o.p) + (at(o, c) + (r0 + (lane >> 3)) * o.rs) * e + k * 16;
+    const int cols = a.C - c - k * per;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i, p += 4 * o.rs * e) {
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (r0 + 4 * i + (lane >> 3) < a.R && cols > 0) x[i] = ld_chunk(o, p, cols);
+    }
+}
+__device__ __forceinline__ void to_stage(uint32_t stage, int lane, const uint4* x) {
+    #pragma unroll
+    for (int i = 0; i < 8; ++i)
+        st_shared_v4(stage + swz128(4 * i + (lane >> 3), lane & 7), x[i].x, x[i].y, x[i].z, x[i].w);
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+// The stage's rows of 8 * CHUNKS bf16 to the kept z.
+__device__ __forceinline__ void pre_out(const Args& a, uint32_t stage, int64_t r0, int c, int lane, int chunks) {
+    const Out& o = a.pre;
+    __nv_bfloat16* base = static_cast<__nv_bfloat16*>(o.p) + at(o, c);
+    const int sh = chunks == 8 ? 3 : 2;
+    for (int i = 0; i < chunks; ++i) {
+        const int row = (lane + 32 * i) >> sh, k = lane & (chunks - 1), cols = a.C - c - k * 8;
+        const uint4 x = ld_shared_v4(stage + swz128(row, k));
+        if (r0 + row >= a.R || cols <= 0) continue;
+        __nv_bfloat16* p = base + (r0 + row) * o.rs + k * 8;
+        if (cols >= 8) {
+            *reinterpret_cast<uint4*>(p) = x;
+        } else {
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            #pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (j < cols) reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+        }
+    }
+}
+// The lane's own row of the stage, 32 columns from column `from` of the piece on, added to z.
+__device__ __forceinline__ void add_own(bool f32, uint32_t stage, int lane, int from, float* z) {
+    if (f32) {
+        #pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint4 x = ld_shared_v4(stage + swz128(lane, from / 4 + k));
+            z[4 * k] += __uint_as_float(x.x); z[4 * k + 1] += __uint_as_float(x.y);
+            z[4 * k + 2] += __uint_as_float(x.z); z[4 * k + 3] += __uint_as_float(x.w);
+        }
+    } else {
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint4 x = ld_shared_v4(stage + swz128(lane, from / 8 + k));
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                z[8 * k + 2 * e] += __uint_as_float(u[e] << 16);
+                z[8 * k + 2 * e + 1] += __uint_as_float(u[e] & 0xffff0000u);
+            }
+        }
+    }
+}
+__device__ __forceinline__ void put_bf16(uint32_t stage, int lane, int from, const float* z) {
+    #pragma unroll
+    for (int k = 0; k < 4; ++k)
+        st_shared_v4(stage + swz128(lane, from / 8 + k), pack_bf16(z[8 * k], z[8 * k + 1]), pack_bf16(z[8 * k + 2], z[8 * k + 3]),
+                     pack_bf16(z[8 * k + 4], z[8 * k + 5]), pack_bf16(z[8 * k + 6], z[8 * k + 7]));
+}
+__device__ __forceinline__ void put_own(bool f32, uint32_t stage, int lane, int from, const float* z) {
+    if (f32) {
+        #pragma unroll
+        for (int k = 0; k < 8; ++k)
+            st_shared_v4(stage + swz128(lane, from / 4 + k), __float_as_uint(z[4 * k]), __float_as_uint(z[4 * k + 1]),
+                         __float_as_uint(z[4 * k + 2]), __float_as_uint(z[4 * k + 3]));
+    } else {
+        put_bf16(stage, lane, from, z);
+    }
+}
+// The lane's row of sums before the first product: residual (through the stage, every load in
+// flight before the first is used) and bias.
+__device__ __forceinline__ void first_sums(const Args& a, float* v, uint32_t stage, int64_t r0, int c0, int lane) {
+    if (a.res.p && c0 < a.C) {
+        const bool f32 = a.res.f32;
+        uint4 x[8], y[8];
+        rows_in(a, r0, c0, lane, x);
+        if (f32) rows_in(a, r0, c0 + 32, lane, y);     // (columns from C on are zero)
+        if (lane == 0) bulk_wait_read0();              // the stage's last store has read it
+        __syncwarp();
+        to_stage(stage, lane, x);
+        __syncwarp();
+        #pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        add_own(f32, stage, lane, 0, v);
+        if (f32) {
+            __syncwarp();
+            to_stage(stage, lane, y);
+            __syncwarp();
+        }
+        #pragma unroll
+        for (int e = 32; e < 64; ++e) v[e] = 0.f;
+        add_own(f32, stage, lane, f32 ? 0 : 32, v + 32);
+    } else {
+        #pragma unroll
+        for (int e = 0; e < 64; ++e) v[e] = 0.f;
+    }
+    #pragma unroll
+    for (int e = 0; e < 64; e += 8) {
+        const int n = min(8, a.C - (c0 + e));
+        if (n > 0) finish<8, false, false>(a, v + e, r0 + lane, c0 + e, n);
+    }
+}
+
 // Lanes are rows of C.  Grid: pairs (CG 2) walk the tiles; or a cluster of `split` CTAs per tile.
-// Three epilogues, so that each keeps its registers:
+// Four epilogues for pairs, so that each keeps its registers, and one that has all for single CTAs:
 //   kSingle  one chunk, rows at 16-byte alignment: straight from the accumulator's columns.
 //   kDirect  several chunks, no activation, no kept z, the same alignment.  The registers' sums
 //            start from bias and residual, read while the first chunk runs, and leave from the
 //            registers, and the last accumulator is handed back as soon as it is added: with the
 //            residual read after the last chunk that held its accumulator longer than the next
-//            chunk lasted (783 cycles per stage instead of 628 with an fp32 residual).
-//   kGeneral the rest: sums of chunks go back to the last one's columns and leave from there; rows
-//            of any alignment; single CTAs.
-constexpr int kSingle = 0, kDirect = 1, kGeneral = 2;
+//            chunk lasted (783 cycles per stage instead of 602 with an fp32 residual).
+//   kSums    several chunks, the same alignment: their sum goes back to the last one's columns and
+//            leaves from there like a single chunk's.
+//   kRows    rows of any alignment.
+constexpr int kSingle = 0, kDirect = 1, kSums = 2, kRows = 3, kAll = 4;
 template <int CG, int BN, int MODE>
 __global__ void __launch_bounds__(Cfg<CG, BN>::kThreads, 1)
 k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
@@ -858,47 +966,33 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
         const bool parts = CG == 1 && a.split > 1;
         int ac = 0;
         bool ok = true;
-        // 32 columns from c on (e of the warp's), finished, into the outgoing stage; a full row of it leaves
-        auto send = [&](int e, int c, int64_t r0, const float* z) {
-            // 32 columns are a whole row of the stage, or half of one of 64 bf16
-            const bool begin = a.y.f32 || !(e & 32), end = a.y.f32 || (e & 32) || c + 32 >= a.C;
-            if (begin) {
-                if (lane == 0) bulk_wait_read0();              // the stage's last store has read it
-                __syncwarp();
-            }
-            if (a.y.f32) {
-                #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    st_shared_v4(stage + swz128(lane, k), __float_as_uint(z[4 * k]), __float_as_uint(z[4 * k + 1]),
-                                 __float_as_uint(z[4 * k + 2]), __float_as_uint(z[4 * k + 3]));
-            } else {
-                #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    st_shared_v4(stage + swz128(lane, (e & 32) / 8 + k), pack_bf16(z[8 * k], z[8 * k + 1]), pack_bf16(z[8 * k + 2], z[8 * k + 3]),
-                                 pack_bf16(z[8 * k + 4], z[8 * k + 5]), pack_bf16(z[8 * k + 6], z[8 * k + 7]));
-            }
-            if (end) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    // what lies outside C is not written
-                    const int cs = a.y.f32 ? c : c & ~63;
-                    const int zh = a.y.hd ? cs / a.y.hd : 0;
-                    tma_store_3d(&tm_y, stage, cs - zh * a.y.hd, (int)r0, zh);
-                    bulk_commit();
-                }
+        // the stage's 32 rows from column c on leave; what lies outside C is not written
+        auto leave = [&](int c, int64_t r0) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                const int zh = a.y.hd ? c / a.y.hd : 0;
+                tma_store_3d(&tm_y, stage, c - zh * a.y.hd, (int)r0, zh);
+                bulk_commit();
             }
         };
+        auto stage_free = [&]() {
+            if (lane == 0) bulk_wait_read0();                  // its last store has read it
+            __syncwarp();
+        };
+        const int piece = a.y.f32 ? 32 : 64;                   // columns of a stage's row
         for (int t = w.first; ok && t < w.ntiles; t += w.step) {
             int tc, tr;
             tile_at(a, t, tc, tr);
             const int64_t r0 = (int64_t)tr * F::kM + (CG == 2 ? 128 * (int)w.rank : 0) + q * 32;
             const int c0 = tc * BN + half * H;
             int buf = ac & 1;
-            if (DIRECT || (MODE == kGeneral && (w.nch > 1 || parts))) {
+            uint4 res[8];
+            if (MODE == kSingle && a.res.p && c0 < a.C) rows_in(a, r0, c0, lane, res);     // while the products run
+            if (DIRECT || (MODE != kSingle && (w.nch > 1 || parts))) {
                 // the chunks add up in registers
                 float v[H];
-                if (DIRECT) first_sums<H>(a, v, r0 + lane, c0);
+                if (DIRECT) first_sums(a, v, stage, r0, c0, lane);
                 for (int ch = 0; ch < w.nch; ++ch, ++ac) {
                     buf = ac & 1;
                     if (!warp_wait(&sm.acc_full[buf], (ac / 2) & 1, a.err, 3301)) { ok = false; break; }
@@ -908,9 +1002,17 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                 }
                 if (!ok) break;
                 if (DIRECT) {
-                    #pragma unroll
-                    for (int e = 0; e < H; e += 32)
-                        if (c0 + e < a.C) send(e, c0 + e, r0, v + e);
+                    if (c0 < a.C) {
+                        stage_free();
+                        put_own(a.y.f32, stage, lane, 0, v);
+                        if (!a.y.f32) put_bf16(stage, lane, 32, v + 32);
+                        leave(c0, r0);
+                    }
+                    if (a.y.f32 && c0 + 32 < a.C) {
+                        stage_free();
+                        put_own(true, stage, lane, 0, v + 32);
+                        leave(c0 + 32, r0);
+                    }
                     continue;
                 }
                 if (parts) {
@@ -932,29 +1034,64 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                 tc_fence_after();
                 ++ac;
             }
-            #pragma unroll 1
-            for (int e = 0; e < H; e += 32) {
-                const int c = c0 + e, n = min(32, a.C - c);
-                if (n <= 0) break;
+            auto load32 = [&](int e, float* z) {
                 uint32_t u[32];
                 PRISM_TMEM_LD32(at0 + buf * BN + e, u);
                 tmem_wait_ld();
-                // the accumulator is free once its last columns are in registers
-                if (e + 32 >= H || c + 32 >= a.C) release<CG>(sm, buf, lane);
-                float z[32];
                 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
-                if (MODE != kGeneral || a.fast) {
-                    finish<32>(a, z, r0 + lane, c, n);
-                    send(e, c, r0, z);
-                    __syncwarp();
-                } else {
-                    // rows at any alignment: turned in the stage, so that a row's columns lie in the lanes
-                    // (a lane writing along its own row took 7.1 ms where this takes 2.1, 24,743 rows of
-                    // 1,904 by 13,119)
+            };
+            if (MODE != kRows && (MODE != kAll || a.fast)) {
+                #pragma unroll 1
+                for (int e = 0; e < H; e += piece) {
+                    const int c = c0 + e;
+                    if (c >= a.C) break;
+                    if (a.res.p && (MODE != kSingle || e)) rows_in(a, r0, c, lane, res);
+                    stage_free();
+                    if (a.pre.p) {
+                        // the kept z has the operands' 16 bits: the backward forms dz from it for 16-bit products
+                        #pragma unroll 1
+                        for (int k = 0; k < piece && c + k < a.C; k += 32) {
+                            float z[32];
+                            load32(e + k, z);
+                            finish<32, false, false>(a, z, r0 + lane, c + k, min(32, a.C - c - k));
+                            put_bf16(stage, lane, k, z);
+                        }
+                        __syncwarp();
+                        pre_out(a, stage, r0, c, lane, piece / 8);
+                        __syncwarp();
+                    }
+                    if (a.res.p) {
+                        to_stage(stage, lane, res);
+                        __syncwarp();
+                    }
+                    #pragma unroll 1
+                    for (int k = 0; k < piece && c + k < a.C; k += 32) {
+                        float z[32];
+                        load32(e + k, z);
+                        // the accumulator is free once its last columns are in registers
+                        if (e + k + 32 >= H || c + k + 32 >= a.C) release<CG>(sm, buf, lane);
+                        finish<32, false, false>(a, z, r0 + lane, c + k, min(32, a.C - c - k));
+                        activate<32>(z, a.act);
+                        if (a.res.p) add_own(a.y.f32, stage, lane, k, z);
+                        put_own(a.y.f32, stage, lane, k, z);
+                    }
+                    leave(c, r0);
+                }
+            } else {
+                // rows at any alignment: turned in the stage, so that a row's columns lie in the lanes
+                // (a lane writing along its own row took 7.1 ms where this takes 2.1, 24,743 rows of
+                // 1,904 by 13,119)
+                #pragma unroll 1
+                for (int e = 0; e < H && c0 + e < a.C; e += 32) {
+                    const int c = c0 + e;
+                    float z[32];
+                    load32(e, z);
+                    if (e + 32 >= H || c + 32 >= a.C) release<CG>(sm, buf, lane);
                     #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        st_shared_v4(stage + swz128(lane, k), u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+                        st_shared_v4(stage + swz128(lane, k), __float_as_uint(z[4 * k]), __float_as_uint(z[4 * k + 1]),
+                                     __float_as_uint(z[4 * k + 2]), __float_as_uint(z[4 * k + 3]));
                     __syncwarp();
                     const Lane l = lane_of(a, c + lane);
                     #pragma unroll 1
@@ -1340,10 +1477,14 @@ static int start_kernel(void (*kernel)(P...), int64_t ctas, int group, int threa
 template <int CG, int BN>
 static int launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty, const Args& a, cudaStream_t s) {
     const int64_t tiles = (int64_t)a.tiles_c * a.tiles_r;
-    void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, Args) = k_tile<CG, BN, kGeneral>;
+    void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, Args);
     if constexpr (CG == 2) {
-        if (a.fast && a.kblocks <= a.chunk) kernel = k_tile<CG, BN, kSingle>;
-        else if (a.fast && a.act == PRISM_ACT_NONE && !a.pre.p) kernel = k_tile<CG, BN, kDirect>;
+        if (!a.fast) kernel = k_tile<CG, BN, kRows>;
+        else if (a.kblocks <= a.chunk) kernel = k_tile<CG, BN, kSingle>;
+        else if (a.act == PRISM_ACT_NONE && !a.pre.p) kernel = k_tile<CG, BN, kDirect>;
+        else kernel = k_tile<CG, BN, kSums>;
+    } else {
+        kernel = k_tile<CG, BN, kAll>;
     }
     return start_kernel(kernel, CG == 2 ? 2 * (tiles < 74 ? tiles : 74) : tiles * a.split, CG == 2 ? 2 : a.split,
                         Cfg<CG, BN>::kThreads, tile_smem<CG, BN>(), s, ta, tb, ty, a);
