@@ -800,45 +800,13 @@ template <int CG, int BN>
 constexpr int tile_smem() { return Cfg<CG, BN>::kRing + Cfg<CG, BN>::kEpi * kStageOut + 1024; }
 constexpr int kPartPitch = 132;            // floats per row of a part (CG 1): rows start 4 banks apart
 
-// A warp's 32 rows of 128 bytes (64 bf16 or 32 fp32 columns from c on) between memory and its
-// stage: eight lanes take a row, so an access touches four lines; a lane reading along its own row
-// touched thirty-two.  Chunks of 16 bytes; one that reaches over C's edge goes element by element.
-__device__ __forceinline__ uint4 ld_chunk(const Out& o, const char* p, int cols) {
-    if (cols >= (o.f32 ? 4 : 8)) return *reinterpret_cast<const uint4*>(p);
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (o.f32) {
-        #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (i < cols) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-    } else {
-        #pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < cols) w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void rows_in(const Args& a, int64_t r0, int c, int lane, uint4* x) {
-    const Out& o = a.res;
-    const int e = o.f32 ? 4 : 2, k = lane & 7, per = 16 / e;
-    const char* p = static_cast<const char*>(o.p) + (at(o, c) + (r0 + (lane >> 3)) * o.rs) * e + k * 16;
-    const int cols = a.C - c - k * per;
-    #pragma unroll
-    for (int i = 0; i < 8; ++i, p += 4 * o.rs * e) {
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (r0 + 4 * i + (lane >> 3) < a.R && cols > 0) x[i] = ld_chunk(o, p, cols);
-    }
-}
-__device__ __forceinline__ void to_stage(uint32_t stage, int lane, const uint4* x) {
-    #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        st_shared_v4(stage + swz128(4 * i + (lane >> 3), lane & 7), x[i].x, x[i].y, x[i].z, x[i].w);
-}
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
-// The stage's rows of 8 * CHUNKS bf16 to the kept z.
+// The stage's rows of 8 `chunks` bf16 to the kept z, `chunks` lanes to a row (an access touches four
+// lines or eight; a lane writing along its own row touched thirty-two).
 __device__ __forceinline__ void pre_out(const Args& a, uint32_t stage, int64_t r0, int c, int lane, int chunks) {
     const Out& o = a.pre;
     __nv_bfloat16* base = static_cast<__nv_bfloat16*>(o.p) + at(o, c);
@@ -896,39 +864,41 @@ __device__ __forceinline__ void put_own(bool f32, uint32_t stage, int lane, int 
         put_bf16(stage, lane, from, z);
     }
 }
-// The lane's row of sums before the first product: residual (through the stage, every load in
-// flight before the first is used) and bias.
-__device__ __forceinline__ void first_sums(const Args& a, float* v, uint32_t stage, int64_t r0, int c0, int lane) {
-    if (a.res.p && c0 < a.C) {
-        const bool f32 = a.res.f32;
-        uint4 x[8], y[8];
-        rows_in(a, r0, c0, lane, x);
-        if (f32) rows_in(a, r0, c0 + 32, lane, y);     // (columns from C on are zero)
-        if (lane == 0) bulk_wait_read0();              // the stage's last store has read it
+// A warp's residual pieces, brought into its stage by TMA (plain loads of them were limited by the
+// little L1 that the ring leaves: 38,701 x 504 x 17,056 in fp32 takes 1.5 ms, took 2.1).  One load
+// at a time.
+struct Residual {
+    const void* tm;
+    uint64_t* bar;
+    uint32_t stage;
+    int issued = 0, waited = 0;
+    // the stage must be free; every lane's accesses to it come first
+    __device__ __forceinline__ void issue(const Args& a, int64_t r0, int c, int lane) {
+        fence_proxy_async_smem();
         __syncwarp();
-        to_stage(stage, lane, x);
-        __syncwarp();
-        #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0.f;
-        add_own(f32, stage, lane, 0, v);
-        if (f32) {
-            __syncwarp();
-            to_stage(stage, lane, y);
-            __syncwarp();
+        if (lane == 0) {
+            const int zh = a.res.hd ? c / a.res.hd : 0;
+            mbar_expect_tx(bar, 4096);
+            asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                         " [%0], [%1, {%3, %4, %5}], [%2];"
+                         :: "r"(stage), "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(c - zh * a.res.hd),
+                            "r"((int)r0), "r"(zh) : "memory");
         }
-        #pragma unroll
-        for (int e = 32; e < 64; ++e) v[e] = 0.f;
-        add_own(f32, stage, lane, f32 ? 0 : 32, v + 32);
-    } else {
-        #pragma unroll
-        for (int e = 0; e < 64; ++e) v[e] = 0.f;
+        ++issued;
     }
-    #pragma unroll
-    for (int e = 0; e < 64; e += 8) {
-        const int n = min(8, a.C - (c0 + e));
-        if (n > 0) finish<8, false, false>(a, v + e, r0 + lane, c0 + e, n);
+    __device__ __forceinline__ bool wait(const Args& a) {
+        const bool ok = warp_wait(bar, waited & 1, a.err, 3302);
+        waited += ok;
+        return ok;
     }
-}
+    // a load that a warp which gave up has not waited for
+    __device__ __forceinline__ void drain() {
+        const uint64_t t0 = globaltimer_ns();
+        if (issued != waited)
+            while (!mbar_try(bar, waited & 1) && globaltimer_ns() - t0 < kWaitNs / 10) {}
+        __syncwarp();
+    }
+};
 
 // Lanes are rows of C.  Grid: pairs (CG 2) walk the tiles; or a cluster of `split` CTAs per tile.
 // Four epilogues for pairs, so that each keeps its registers, and one that has all for single CTAs:
@@ -937,7 +907,7 @@ __device__ __forceinline__ void first_sums(const Args& a, float* v, uint32_t sta
 //            start from bias and residual, read while the first chunk runs, and leave from the
 //            registers, and the last accumulator is handed back as soon as it is added: with the
 //            residual read after the last chunk that held its accumulator longer than the next
-//            chunk lasted (783 cycles per stage instead of 602 with an fp32 residual).
+//            chunk lasted (783 cycles per stage instead of 563 with an fp32 residual).
 //   kSums    several chunks, the same alignment: their sum goes back to the last one's columns and
 //            leaves from there like a single chunk's.
 //   kRows    rows of any alignment.
@@ -945,14 +915,17 @@ constexpr int kSingle = 0, kDirect = 1, kSums = 2, kRows = 3, kAll = 4;
 template <int CG, int BN, int MODE>
 __global__ void __launch_bounds__(Cfg<CG, BN>::kThreads, 1)
 k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-       const __grid_constant__ CUtensorMap tm_y, const Args a) {
+       const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r, const Args a) {
     using F = Cfg<CG, BN>;
     constexpr int ST = F::kStages, H = F::kCol;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<ST> sm;
+    __shared__ uint64_t res_full[F::kEpi];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const Work w = work_of<CG>(a);
+    if (threadIdx.x == 0)
+        for (int i = 0; i < F::kEpi; ++i) mbar_init(&res_full[i], 1);
     const uint32_t tmem = start<CG, BN, ST>(sm, warp);
     if (warp == F::kEpi) {
         produce<CG, BN, true, ST>(&tm_a, &tm_b, a, w, sm, ring);
@@ -981,18 +954,40 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
             __syncwarp();
         };
         const int piece = a.y.f32 ? 32 : 64;                   // columns of a stage's row
+        Residual res{&tm_r, &res_full[warp], stage};
         for (int t = w.first; ok && t < w.ntiles; t += w.step) {
             int tc, tr;
             tile_at(a, t, tc, tr);
             const int64_t r0 = (int64_t)tr * F::kM + (CG == 2 ? 128 * (int)w.rank : 0) + q * 32;
             const int c0 = tc * BN + half * H;
             int buf = ac & 1;
-            uint4 res[8];
-            if (MODE == kSingle && a.res.p && c0 < a.C) rows_in(a, r0, c0, lane, res);     // while the products run
+            if (MODE == kSingle && a.res.p && !a.pre.p && c0 < a.C) {                      // while the products run
+                stage_free();
+                res.issue(a, r0, c0, lane);
+            }
             if (DIRECT || (MODE != kSingle && (w.nch > 1 || parts))) {
                 // the chunks add up in registers
                 float v[H];
-                if (DIRECT) first_sums(a, v, stage, r0, c0, lane);
+                if (DIRECT) {
+                    #pragma unroll
+                    for (int e = 0; e < H; ++e) v[e] = 0.f;
+                    #pragma unroll
+                    for (int e = 0; e < H; e += 32)
+                        if (a.res.p && ok && c0 + e < a.C) {
+                            if (e == 0) stage_free();
+                            if (e == 0 || a.y.f32) {
+                                res.issue(a, r0, c0 + e, lane);
+                                ok = res.wait(a);
+                            }
+                            if (ok) add_own(a.y.f32, stage, lane, a.y.f32 ? 0 : e, v + e);
+                        }
+                    if (!ok) break;
+                    #pragma unroll
+                    for (int e = 0; e < H; e += 8) {
+                        const int n = min(8, a.C - (c0 + e));
+                        if (n > 0) finish<8, false, false>(a, v + e, r0 + lane, c0 + e, n);
+                    }
+                }
                 for (int ch = 0; ch < w.nch; ++ch, ++ac) {
                     buf = ac & 1;
                     if (!warp_wait(&sm.acc_full[buf], (ac / 2) & 1, a.err, 3301)) { ok = false; break; }
@@ -1046,8 +1041,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                 for (int e = 0; e < H; e += piece) {
                     const int c = c0 + e;
                     if (c >= a.C) break;
-                    if (a.res.p && (MODE != kSingle || e)) rows_in(a, r0, c, lane, res);
-                    stage_free();
+                    if (res.issued == res.waited) stage_free();
                     if (a.pre.p) {
                         // the kept z has the operands' 16 bits: the backward forms dz from it for 16-bit products
                         #pragma unroll 1
@@ -1062,8 +1056,8 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                         __syncwarp();
                     }
                     if (a.res.p) {
-                        to_stage(stage, lane, res);
-                        __syncwarp();
+                        if (res.issued == res.waited) res.issue(a, r0, c, lane);
+                        if (!res.wait(a)) { ok = false; break; }
                     }
                     #pragma unroll 1
                     for (int k = 0; k < piece && c + k < a.C; k += 32) {
@@ -1108,6 +1102,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
             }
             if (c0 >= a.C) release<CG>(sm, buf, lane);         // (a tile's half without columns)
         }
+        res.drain();
         if (lane == 0) bulk_wait0();
     }
     if (CG == 1 && a.split > 1) {
@@ -1397,7 +1392,7 @@ static int make_operand(CUtensorMap* m, Operand* o, const Matrix& x, bool mn, in
     return r == CUDA_SUCCESS ? PRISM_OK : PRISM_ERR_CUDA;
 }
 
-// C as boxes of 32 rows by 128 bytes.
+// C, or a residual of its shape, as boxes of 32 rows by 128 bytes.
 static int make_out_map(CUtensorMap* m, const Out& y, int64_t R, int C) {
     auto enc = encode_fn();
     if (!enc) return PRISM_ERR_CUDA;
@@ -1475,9 +1470,10 @@ static int start_kernel(void (*kernel)(P...), int64_t ctas, int group, int threa
 }
 
 template <int CG, int BN>
-static int launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty, const Args& a, cudaStream_t s) {
+static int launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty, const CUtensorMap& tr,
+                       const Args& a, cudaStream_t s) {
     const int64_t tiles = (int64_t)a.tiles_c * a.tiles_r;
-    void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, Args);
+    void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Args);
     if constexpr (CG == 2) {
         if (!a.fast) kernel = k_tile<CG, BN, kRows>;
         else if (a.kblocks <= a.chunk) kernel = k_tile<CG, BN, kSingle>;
@@ -1487,7 +1483,7 @@ static int launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const CUten
         kernel = k_tile<CG, BN, kAll>;
     }
     return start_kernel(kernel, CG == 2 ? 2 * (tiles < 74 ? tiles : 74) : tiles * a.split, CG == 2 ? 2 : a.split,
-                        Cfg<CG, BN>::kThreads, tile_smem<CG, BN>(), s, ta, tb, ty, a);
+                        Cfg<CG, BN>::kThreads, tile_smem<CG, BN>(), s, ta, tb, ty, tr, a);
 }
 template <int BN>
 static int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const Args& a, cudaStream_t s) {
@@ -1520,14 +1516,15 @@ static int product(const Matrix& X, bool x_mn, const Matrix& Y, bool y_mn, int64
     if (sh.few)
         return sh.bn == 16 ? launch_few<16>(ty, tx, a, s) : sh.bn == 32 ? launch_few<32>(ty, tx, a, s) : launch_few<64>(ty, tx, a, s);
     // a map of C wants its address and row stride in whole 16 bytes
-    CUtensorMap to{};
+    CUtensorMap to{}, tr2{};
     a.fast = a.y.vec && (!a.res.p || a.res.vec) && (!a.pre.p || a.pre.vec);
     if (a.fast) st = make_out_map(&to, a.y, R, C);
+    if (!st && a.fast && a.res.p) st = make_out_map(&tr2, a.res, R, C);
     if (st) return st;
-    if (sh.cg == 1) return launch_tile<1, 128>(tx, ty, to, a, s);
-    return sh.bn == 256   ? launch_tile<2, 256>(tx, ty, to, a, s)
-           : sh.bn == 192 ? launch_tile<2, 192>(tx, ty, to, a, s)
-                          : launch_tile<2, 128>(tx, ty, to, a, s);
+    if (sh.cg == 1) return launch_tile<1, 128>(tx, ty, to, tr2, a, s);
+    return sh.bn == 256   ? launch_tile<2, 256>(tx, ty, to, tr2, a, s)
+           : sh.bn == 192 ? launch_tile<2, 192>(tx, ty, to, tr2, a, s)
+                          : launch_tile<2, 128>(tx, ty, to, tr2, a, s);
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

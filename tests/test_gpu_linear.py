@@ -88,6 +88,9 @@ def test_forward_exact(name, out, cuda_device):
     got, pre, st = _lib.linear(x, W, out_heads=oh, out_dtype=out, status=st)
     _ok(st)
     assert pre is None and torch.equal(got, ref.heads(want - b.double(), oh).to(out))
+    got, pre, st = _lib.linear(x, W, b, r, out_heads=oh, status=st)
+    _ok(st)
+    assert pre is None and torch.equal(got, (ref.heads(want, oh) + r.double()).to(out))
 
 
 @pytest.mark.parametrize("name", list(SHAPES))
@@ -179,11 +182,13 @@ def test_weight_gradient_over_many_rows(cuda_device):
     assert bool(((db.double() - sums).abs() <= (M / 8 / 8 + 16) * ref.EPS32 * dy.double().abs().sum(0)).all())
 
 
-def test_residual_in_place(cuda_device):
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+def test_residual_in_place(dt, cuda_device):
     g = _gen(6)
-    for M, K, N in ((5, 640, 256), (100, 100, 130), (2600, 128, 2100)):
-        x, W, r = _ints((M, K), g), _ints((N, K), g), _ints((M, N), g, 99, F32)
-        want = (x.double() @ W.double().t() + r.double()).float()
+    for M, K, N in ((5, 640, 256), (100, 100, 130), (100, 2000, 136), (2600, 128, 2100), (2600, 2000, 2104), (2600, 900, 2101),
+                    (2570, 17000, 2048)):
+        x, W, r = _ints((M, K), g), _ints((N, K), g), _ints((M, N), g, 99, dt)
+        want = (x.double() @ W.double().t() + r.double()).to(dt)
         y, _, st = _lib.linear(x, W, residual=r, y=r)
         _ok(st)
         assert y is r and torch.equal(r, want)
