@@ -111,8 +111,7 @@ template <> struct Vec8<float> {
 // Sums of U rows' values over the LANES lanes that hold a row: s[i] is this lane's part of row
 // i.  Each exchange halves the rows a lane still carries, so U rows cost U - 1 + log2(LANES / U)
 // shuffles instead of U log2(LANES); what follows from a row's sum is computed by the lanes that
-// own the row, owned_row() of them, and handed to all by from_owner().
-template <int U> __device__ __forceinline__ int owned_row(int lane) { return lane & (U - 1); }
+// own the row (lane & (U - 1) is its number) and handed to all by from_owner().
 template <int LANES, int U>
 __device__ __forceinline__ float owned_sum(const float* s, int lane) {
     static_assert(U == 1 || U == 2 || U == 4, "rows of a group");
