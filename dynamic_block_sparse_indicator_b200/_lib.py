@@ -642,7 +642,10 @@ def make_rope(T, H, W, dims, theta=10000.0, pairing=PRISM_PAIR_ADJACENT, first_f
     if len(dims) != 3 or any(d < 0 or d % 2 for d in dims) or min(T, H, W) < 1:
         raise ValueError(f"dims must be three even counts of channels and T, H, W positive, got {dims} and {(T, H, W)}")
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    table = torch.empty(max(T * dims[0] + H * dims[1] + W * dims[2], 4), dtype=torch.float32, device=dev)
+    with torch.cuda.stream(stream):          # (None: the current one)
+        table = torch.empty(max(T * dims[0] + H * dims[1] + W * dims[2], 4), dtype=torch.float32, device=dev)
+    if stream is not None:                   # (its memory is that stream's, its readers the current one)
+        table.record_stream(torch.cuda.current_stream(dev))
     rope = Rope(table, int(T), int(H), int(W), dims, int(pairing))
     D = 64 if sum(dims) <= 64 else 128
     p = _norm_rope_params(T * H * W, 1, D, PRISM_BF16, PRISM_BF16, PRISM_F32, rope, 1.0)

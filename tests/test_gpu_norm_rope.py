@@ -262,3 +262,18 @@ def test_refusals_on_the_device(cuda_device):
                  lambda: _lib.qk_norm_rope(x, None, torch.ones(64))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_table_on_another_stream_takes_no_memory_in_use(cuda_device):
+    """A table made on a stream is not laid over a freed tensor that the current stream still writes."""
+    T, H, W, dims = 7, 30, 52, (44, 42, 42)
+    want = _lib.make_rope(T, H, W, dims).table.clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    old = torch.empty_like(want)
+    for _ in range(200):                 # (the current stream is behind)
+        old.fill_(7.0)
+    del old
+    rope = _lib.make_rope(T, H, W, dims, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(rope.table, want)
