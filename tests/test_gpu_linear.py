@@ -218,6 +218,26 @@ def test_bad_values_stay_in_their_rows(cuda_device):
         assert torch.equal(got[keep], clean[keep])
 
 
+@pytest.mark.parametrize("act", [GELU, TANH, SILU])
+@pytest.mark.parametrize("cols", [256, 251])
+def test_derivative_far_out(act, cols, cuda_device):
+    """act' from -3e4 to 3e4, 0 and +-tiny included: dy = 1 and W the identity, so dx is act'(z) rounded once."""
+    g = _gen(11)
+    z = torch.cat([torch.tensor([0.0, -0.0, 1e-30, -1e-30, 3e4, -3e4, 1e3, -1e3, 120.0, -120.0], device="cuda"),
+                   torch.linspace(-14, 14, 4000, device="cuda"),
+                   torch.randn(40 * cols - 4010, generator=g, device="cuda") * 50]).to(BF).reshape(40, cols)
+    dy, eye = torch.ones(40, cols, device="cuda", dtype=BF), torch.eye(cols, device="cuda", dtype=BF)
+    dx, _, db, st = _lib.linear_bwd(dy, dy, eye, z, act)
+    _ok(st)
+    want = ref.act_grad(z.double(), act)
+    err = 32 * ref.EPS32 * (z.double().abs() + 1)
+    # where the derivative is 0 or 1 to 32 bits nothing is lost: s = 0 or 1 exactly
+    err = torch.where(z.double().abs() > 20, 1e-7, err)
+    assert bool(((dx.double() - want).abs() <= ref.half(BF) * (want.abs() + err) + err).all())
+    # the sums: of unrounded values, 39 fp32 additions of values below 1.2
+    assert bool(((db.double() - want.sum(0)).abs() <= err.sum(0) + 39 * ref.EPS32 * 1.2 * 40).all())
+
+
 def test_same_bits_twice_and_under_a_graph(cuda_device):
     g = _gen(8)
     for M, K, N in ((3, 4096, 512), (300, 520, 777), (2600, 520, 2100)):
