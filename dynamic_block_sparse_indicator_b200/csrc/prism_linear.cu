@@ -544,17 +544,20 @@ __device__ __forceinline__ void produce(const void* tm_a, const void* tm_b, cons
             if (++s == ST) { s = 0; ++round; }
         }
     }
-    // every copy has landed before the block may end: after a wait that gave up, too (then for at
-    // most a tenth of a second)
-    if (CG == 1 || w.rank == 0) {
-        const uint64_t t0 = globaltimer_ns();
-        for (int i = 0; i < ST; ++i) {
-            const int uses = round + (i < s ? 1 : 0);
-            if (uses)
-                while (!mbar_try(&sm.full[i], (uses - 1) & 1) && globaltimer_ns() - t0 < kWaitNs / 10) {}
-        }
-        __syncwarp();
+    // Before the block may end, every copy has landed and every product's arrival at this CTA's `empty`
+    // has come: the arrivals of the last stages have no other wait, and in a pair they come from the
+    // other CTA.  (After a wait that gave up, too: then for at most a tenth of a second.)
+    const bool lands = CG == 1 || w.rank == 0;
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 0; i < ST; ++i) {
+        const int uses = round + (i < s ? 1 : 0);
+        if (!uses) continue;
+        const uint32_t par = (uses - 1) & 1;
+        if (lands)
+            while (!mbar_try(&sm.full[i], par) && globaltimer_ns() - t0 < kWaitNs / 10) {}
+        while (!mbar_try(&sm.empty[i], par) && globaltimer_ns() - t0 < kWaitNs / 10) {}
     }
+    __syncwarp();
 }
 
 // The MMA issuer (one warp; of a pair, the first CTA's).
