@@ -655,6 +655,20 @@ static bool apart(const Span& x, const Span& y) {
     return y.lo >= x.lo ? m >= xin && outer - m >= yin : m >= yin && outer - m >= xin;
 }
 
+// Consecutive bytes at `p` (none where it is null).
+static Span flat(const void* p, size_t bytes) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return Span{lo, p ? lo + bytes : lo, 0, 0, 1, 1, p ? (int64_t)bytes : 0};
+}
+static bool clear_of(const Span& x, const Span* others, int n) {
+    for (int i = 0; i < n; ++i)
+        if (others[i].lo != others[i].hi && !apart(x, others[i])) return false;
+    return true;
+}
+static size_t table_bytes(const prism_norm_rope_params* p) {
+    return ((size_t)p->T * p->dim_t + (size_t)p->H * p->dim_h + (size_t)p->W * p->dim_w) * sizeof(float);
+}
+
 static bool same(const Span& x, const Span& y) {
     return x.lo == y.lo && x.hs == y.hs && x.ts == y.ts && x.row == y.row;
 }
@@ -779,6 +793,10 @@ extern "C" int prism_qk_norm_rope(const prism_norm_rope_params* p, const prism_r
         for (int j = 0; j < z; ++j)
             if (!apart(so[i], si[j]) && !(i == j && same(so[i], si[j]))) return PRISM_ERR_INVALID_ARG;
     if (z == 2 && !apart(so[0], so[1])) return PRISM_ERR_INVALID_ARG;
+    const Span read[3] = {flat(wq, (size_t)D * elt(p->w_dtype)), flat(wk, (size_t)D * elt(p->w_dtype)),
+                          flat(rope, rope ? table_bytes(p) : 0)};
+    for (int i = 0; i < z; ++i)
+        if (!clear_of(so[i], read, 3)) return PRISM_ERR_INVALID_ARG;
     if (int st = device_ok()) return st;
     Args a{};
     for (int i = 0; i < z; ++i) {
@@ -818,9 +836,10 @@ extern "C" int prism_qk_norm_rope_bwd(const prism_norm_rope_params* p, const pri
     if (bad_params(p) || !q || !dq_out || !dq || !k != !dk_out || !k != !dk) return PRISM_ERR_INVALID_ARG;
     if ((dwk || wk) && !k) return PRISM_ERR_INVALID_ARG;
     if (!aligned16(wq) || !aligned16(wk) || !aligned16(dwq) || !aligned16(dwk)) return PRISM_ERR_INVALID_ARG;
-    if (dwq && dwq == dwk) return PRISM_ERR_INVALID_ARG;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int D = p->head_dim, z = k ? 2 : 1;
+    const Span both[1] = {flat(dwk, D * sizeof(float))};
+    if (dwq && !clear_of(flat(dwq, D * sizeof(float)), both, 1)) return PRISM_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p->N == 0) {         // no rows: the weights' gradients are zero
         for (float* dw : {dwq, dwk})
             if (dw && cudaMemsetAsync(dw, 0, D * sizeof(float), s) != cudaSuccess) return PRISM_ERR_CUDA;
@@ -848,7 +867,17 @@ extern "C" int prism_qk_norm_rope_bwd(const prism_norm_rope_params* p, const pri
     if (z == 2 && !apart(so[0], so[1])) return PRISM_ERR_INVALID_ARG;
     const bool want = dwq || dwk;
     if (want && (!workspace || !aligned16(workspace))) return PRISM_ERR_INVALID_ARG;
-    if (want && ws_bytes < prism_qk_norm_rope_bwd_workspace_bytes(p)) return PRISM_ERR_WORKSPACE;
+    const size_t need = want ? prism_qk_norm_rope_bwd_workspace_bytes(p) : 0;
+    if (want && ws_bytes < need) return PRISM_ERR_WORKSPACE;
+    // the vectors, the table and the workspace: what is written of them is apart from all else, what
+    // is read from what is written
+    const Span vec[6] = {flat(dwq, D * sizeof(float)), flat(dwk, D * sizeof(float)), flat(want ? workspace : nullptr, need),
+                         flat(wq, (size_t)D * elt(p->w_dtype)), flat(wk, (size_t)D * elt(p->w_dtype)),
+                         flat(rope, rope ? table_bytes(p) : 0)};
+    for (int i = 0; i < z; ++i)
+        if (!clear_of(so[i], vec, 6) || !clear_of(si[i], vec, 3) || !clear_of(sg[i], vec, 3)) return PRISM_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+        if (vec[i].lo != vec[i].hi && !clear_of(vec[i], vec + i + 1, 5 - i)) return PRISM_ERR_INVALID_ARG;
     if (int st = device_ok()) return st;
     Args a{};
     for (int i = 0; i < z; ++i) {

@@ -429,7 +429,8 @@ PRISM_API int prism_status_read(int32_t* dev_status, int32_t* site, void* stream
  *   q_out, k_out   the results' rows; [heads][N][D] with head_stride N D and
  *              token_stride D is what prism_plan reads.  A result may be its own
  *              input (same address, strides and element size); any other
- *              overlap of what is written is refused (PRISM_ERR_INVALID_ARG).
+ *              overlap of what is written, with weights and table too, is
+ *              refused (PRISM_ERR_INVALID_ARG).
  *              Nothing outside the rows is written.
  * prism_rope_table writes that table: angle position theta^(-2 p / d) for pair p
  *   of an axis of d channels, the T axis starting at first_frame (a sequence
@@ -468,7 +469,8 @@ PRISM_API int prism_qk_norm_rope(const prism_norm_rope_params* p, const prism_ro
  *   dq_out, dk_out   gradients by the results (out_dtype rows: what
  *                    prism_attn_bwd writes as dQ, dK);
  *   dq, dk           gradients by q, k (dtype rows, written); each may be its own
- *                    dq_out / dk_out or q / k in place, else nothing may overlap;
+ *                    dq_out / dk_out or q / k in place; any other overlap of what
+ *                    is written (dwq, dwk and the workspace too) is refused;
  *   dwq, dwk         device fp32 [D], gradients by the weights summed over heads
  *                    and tokens, or NULL.  The order of the sums is fixed: the
  *                    same call gives the same bits.

@@ -1,0 +1,77 @@
+"""What the layer's operators write may share no byte with what else a call reads or writes: weights,
+rotation table, weights' gradients, workspace and status block included.  Addresses only; a call that
+passes the checks ends at the missing device (no GPU)."""
+import ctypes as C
+
+import pytest
+import torch
+
+from dynamic_block_sparse_indicator_b200 import _lib
+
+INV = _lib.PRISM_ERR_INVALID_ARG
+N, HEADS, D = 24, 2, 64
+ROWS = HEADS * N * D * 2                                            # bytes of a bf16 tensor of rows
+Q, K, QO, KO, WQ, WK, TAB, DWQ, DWK, WS = ((i + 1) << 24 for i in range(10))
+TABLE = (2 * 16 + 3 * 8 + 4 * 8) * 4
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if torch.cuda.is_available():
+        pytest.skip("addresses that no device may see")
+    from dynamic_block_sparse_indicator_b200 import build
+    build.build_library()
+    return _lib.load()
+
+
+def _norm_params(w_dtype=1):
+    return _lib.PrismNormRopeParams(N, 2, 3, 4, HEADS, D, 0, 0, w_dtype, 16, 8, 8, 0, 1e-6)
+
+
+def _rows(at):
+    return C.byref(_lib.PrismRows(at, N * D, D))
+
+
+def _norm(lib, q=Q, k=K, wq=WQ, wk=WK, tab=TAB, qo=QO, ko=KO):
+    return lib.prism_qk_norm_rope(C.byref(_norm_params()), _rows(q), _rows(k), wq, wk, tab, _rows(qo), _rows(ko), None)
+
+
+def _norm_bwd(lib, dqo=Q, dko=K, q=11 << 24, k=12 << 24, wq=WQ, wk=WK, tab=TAB, dq=QO, dk=KO, dwq=DWQ, dwk=DWK, ws=WS):
+    p = _norm_params()
+    n = lib.prism_qk_norm_rope_bwd_workspace_bytes(C.byref(p))
+    return lib.prism_qk_norm_rope_bwd(C.byref(p), _rows(dqo), _rows(dko), _rows(q), _rows(k), wq, wk, tab, _rows(dq),
+                                      _rows(dk), dwq, dwk, ws, n, None)
+
+
+def _ends(at, size, other):
+    """Addresses at which `other` bytes touch the first and the last 16 bytes of [at, at + size)."""
+    return at + 16 - other, at + size - 16
+
+
+def test_norm(lib):
+    assert _norm(lib) == _lib.PRISM_ERR_UNSUPPORTED
+    for out in (QO, KO):
+        for a in _ends(out, ROWS, D * 4):
+            assert _norm(lib, wq=a) == INV and _norm(lib, wk=a) == INV
+        for a in _ends(out, ROWS, TABLE):
+            assert _norm(lib, tab=a) == INV
+    # beside it, and shared between what is only read
+    assert _norm(lib, wq=QO + ROWS, wk=QO + ROWS, tab=QO - TABLE) == _lib.PRISM_ERR_UNSUPPORTED
+    assert _norm(lib, wq=Q, wk=TAB, tab=TAB) == _lib.PRISM_ERR_UNSUPPORTED
+
+
+def test_norm_gradients(lib):
+    ok = _lib.PRISM_ERR_UNSUPPORTED
+    n = lib.prism_qk_norm_rope_bwd_workspace_bytes(C.byref(_norm_params()))
+    assert _norm_bwd(lib) == ok
+    for name, size in (("wq", D * 4), ("wk", D * 4), ("tab", TABLE), ("dwq", D * 4), ("dwk", D * 4), ("ws", n)):
+        for at, rows in ((QO, ROWS), (KO, ROWS), (DWQ, D * 4), (DWK, D * 4), (WS, n)):
+            if at != dict(dwq=DWQ, dwk=DWK, ws=WS).get(name):
+                for a in _ends(at, rows, size):
+                    assert _norm_bwd(lib, **{name: a}) == INV, (name, at)
+    for name in ("dqo", "dko", "q", "k"):
+        for at, size in ((DWQ, D * 4), (DWK, D * 4), (WS, n)):
+            for a in _ends(at, size, ROWS):
+                assert _norm_bwd(lib, **{name: a}) == INV, (name, at)
+    assert _norm_bwd(lib, dwq=QO + ROWS, dwk=QO + ROWS + D * 4, ws=KO + ROWS) == ok
+    assert _norm_bwd(lib, dwq=None, dwk=None, ws=QO) == ok          # an unused workspace is not looked at
