@@ -1793,6 +1793,11 @@ extern "C" int prism_linear(const prism_linear_params* p, const void* x, const v
     const size_t need = x_bytes(p) + w_bytes(p);
     if (need && !workspace) return PRISM_ERR_INVALID_ARG;
     if (need > ws_bytes) return PRISM_ERR_WORKSPACE;
+    const Span sw = span(need ? workspace : nullptr, 1, (int64_t)need, 0, (int64_t)need, 1);
+    const Span ss = span(dev_status, 1, 4, 0, 4, 4);
+    for (const Span& i : {in[0], in[1], in[2], sr, sy, sp, ss})
+        if (!apart(sw, i)) return PRISM_ERR_INVALID_ARG;
+    if (!apart(ss, sy) || !apart(ss, sp)) return PRISM_ERR_INVALID_ARG;
     if (int st = device_ok()) return st;
     nvtxRangePushA("prism linear");
     const int st = forward(p, x, W, bias, residual, y, pre, static_cast<char*>(workspace), dev_status,
@@ -1839,6 +1844,11 @@ extern "C" int prism_linear_bwd(const prism_linear_params* p, const void* dy, co
     const size_t need = prism_linear_bwd_workspace_bytes(p) - 256;
     if (need && !workspace) return PRISM_ERR_INVALID_ARG;
     if (need > ws_bytes) return PRISM_ERR_WORKSPACE;
+    const Span sw = span(workspace, 1, (int64_t)need, 0, (int64_t)need, 1), ss = span(dev_status, 1, 4, 0, 4, 4);
+    for (const Span& i : {in[0], in[1], in[2], in[3], out[0], out[1], out[2], ss})
+        if (!apart(sw, i)) return PRISM_ERR_INVALID_ARG;
+    for (const Span& o : out)
+        if (!apart(ss, o)) return PRISM_ERR_INVALID_ARG;
     if (int st = device_ok()) return st;
     nvtxRangePushA("prism linear bwd");
     const int st = backward(p, dy, x, W, pre, dx, dW, db, static_cast<char*>(workspace), dev_status, s);

@@ -520,7 +520,8 @@ PRISM_API int prism_qk_norm_rope_bwd(const prism_norm_rope_params* p, const pris
  *              Not to be shared by calls that may overlap in time.
  *   dev_status device int32[4], zero before the call (see prism_av_norm).
  * Sums run in a fixed order: the same call gives the same bits.  What is written
- * may not overlap what else the call reads or writes, y over residual excepted.
+ * (the workspace and the status block too) may not overlap what else the call
+ * reads or writes, y over residual excepted: PRISM_ERR_INVALID_ARG.
  */
 #define PRISM_ACT_NONE      0
 #define PRISM_ACT_GELU      1

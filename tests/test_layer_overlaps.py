@@ -75,3 +75,52 @@ def test_norm_gradients(lib):
                 assert _norm_bwd(lib, **{name: a}) == INV, (name, at)
     assert _norm_bwd(lib, dwq=QO + ROWS, dwk=QO + ROWS + D * 4, ws=KO + ROWS) == ok
     assert _norm_bwd(lib, dwq=None, dwk=None, ws=QO) == ok          # an unused workspace is not looked at
+
+
+# ---- projections: [10][136] by [256][136], the operands packed in the workspace
+M_, K_, N_ = 10, 136, 256
+X, W, B, R, Y, PRE, S, ST, DX, DW, DB = ((i + 1) << 24 for i in range(11))
+
+
+def _linear_params(**kw):
+    base = dict(M=M_, K=K_, N=N_, in_heads=0, out_heads=0, activation=2, out_dtype=0, bias_dtype=1, dw_dtype=1, x_stride=137,
+                w_stride=137, y_stride=N_, r_stride=N_)
+    base.update(kw)
+    return _lib.PrismLinearParams(*[base[f] for f, _ in _lib.PrismLinearParams._fields_])
+
+
+def test_linear(lib):
+    ok, p = _lib.PRISM_ERR_UNSUPPORTED, _linear_params()
+    need = lib.prism_linear_workspace_bytes(C.byref(p)) - 256
+
+    def call(x=X, w=W, b=B, r=R, y=Y, pre=PRE, ws=S, st=ST):
+        return lib.prism_linear(C.byref(p), x, w, b, r, y, pre, ws, need, st, None)
+
+    assert call() == ok
+    sizes = dict(x=(X, ((M_ - 1) * 137 + K_) * 2), w=(W, ((N_ - 1) * 137 + K_) * 2), b=(B, N_ * 4), r=(R, M_ * N_ * 2),
+                 y=(Y, M_ * N_ * 2), pre=(PRE, M_ * N_ * 2))
+    for at, size in sizes.values():
+        for a in (at + 16 - need, at + (size - 1) // 16 * 16):
+            assert call(ws=a) == INV
+    for at, size in (sizes["y"], sizes["pre"], (S, need)):
+        for a in _ends(at, size, 16):
+            assert call(st=a) == INV
+    assert call(ws=Y + M_ * N_ * 2, st=Y - 16) == ok
+
+
+def test_linear_gradients(lib):
+    ok, p = _lib.PRISM_ERR_UNSUPPORTED, _linear_params()
+    need = lib.prism_linear_bwd_workspace_bytes(C.byref(p)) - 256
+
+    def call(dy=Y, x=X, w=W, pre=PRE, dx=DX, dw=DW, db=DB, ws=12 << 24, st=ST):
+        return lib.prism_linear_bwd(C.byref(p), dy, x, w, pre, dx, dw, db, ws, need, st, None)
+
+    assert call() == ok
+    outs = ((DX, M_ * K_ * 2), (DW, N_ * K_ * 4), (DB, N_ * 4))
+    for at, size in ((X, ((M_ - 1) * 137 + K_) * 2), (W, ((N_ - 1) * 137 + K_) * 2), (Y, M_ * N_ * 2), (PRE, M_ * N_ * 2), *outs):
+        for a in (at + 16 - need // 16 * 16, at + (size - 1) // 16 * 16):
+            assert call(ws=a) == INV
+    for at, size in (*outs, (12 << 24, need)):
+        for a in _ends(at, size // 16 * 16, 16):
+            assert call(st=a) == INV
+    assert call(ws=DX + M_ * K_ * 2, st=DW - 16) == ok
