@@ -741,6 +741,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k=None, wq=None, wk=None, rope=None, eps
         raise ValueError("wk without k")
     dt, gdt, wdt = _code(q.dtype, "q"), _code(dq_out.dtype, "dq_out"), _weights((wq, wk), D, "wq and wk")
     table = None if rope is None else rope.table
+    ws_bytes = _size(workspace)
     go = _Launch((q, k, dq_out, dk_out, wq, wk, dq, dk, workspace, table), stream)
 
     def like(x):
@@ -757,10 +758,11 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k=None, wq=None, wk=None, rope=None, eps
     p = _norm_rope_params(N, heads, D, dt, gdt, wdt, rope, eps)
     lib = load()
     if workspace is None and (dwq is not None or dwk is not None):
-        workspace = go.empty((max(int(lib.prism_qk_norm_rope_bwd_workspace_bytes(C.byref(p))), 16),), torch.uint8)
+        ws_bytes = max(int(lib.prism_qk_norm_rope_bwd_workspace_bytes(C.byref(p))), 16)
+        workspace = go.empty((ws_bytes,), torch.uint8)
     go.call("prism_qk_norm_rope_bwd", lib.prism_qk_norm_rope_bwd, C.byref(p), _rows(dq_out, "dq_out"),
             _rows(dk_out, "dk_out"), _rows(q, "q"), _rows(k, "k"), _at(wq), _at(wk), _at(table), _rows(dq, "dq"),
-            _rows(dk, "dk"), _at(dwq), _at(dwk), _at(workspace), _size(workspace))
+            _rows(dk, "dk"), _at(dwq), _at(dwk), _at(workspace), ws_bytes)
     return dq, dk, dwq, dwk
 
 
@@ -794,8 +796,13 @@ def _in_layout(t, what, shape, dtype):
     return _features(t, what, dtype)[3]
 
 
-def _size(t):
-    return 0 if t is None else t.numel() * t.element_size()
+def _size(workspace):
+    """Bytes of a workspace."""
+    if workspace is None:
+        return 0
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
 
 
 def _check_status(t):
@@ -834,6 +841,7 @@ def linear(x, W, bias=None, residual=None, activation=PRISM_ACT_NONE, y=None, ou
     p = PrismLinearParams(M, K, N, in_heads, out_heads, int(activation), _code(out_dtype, "y"),
                           PRISM_F32 if bias is None else _code(bias.dtype, "bias"), PRISM_F32, xs, ws_, y_stride, r_stride)
     _check_status(status)
+    ws_bytes = _size(workspace)
     lib = load()
     go = _Launch((x, W, bias, residual, y, pre, workspace, status), stream)
     if y is None:
@@ -841,11 +849,12 @@ def linear(x, W, bias=None, residual=None, activation=PRISM_ACT_NONE, y=None, ou
     if want_pre and pre is None:
         pre = go.empty(want, torch.bfloat16)
     if workspace is None and (xs % 8 or ws_ % 8):
-        workspace = go.empty((max(int(lib.prism_linear_workspace_bytes(C.byref(p))), 16),), torch.uint8)
+        ws_bytes = max(int(lib.prism_linear_workspace_bytes(C.byref(p))), 16)
+        workspace = go.empty((ws_bytes,), torch.uint8)
     if status is None:
         status = go.zero_status()
     go.call("prism_linear", lib.prism_linear, C.byref(p), x.data_ptr(), W.data_ptr(), _at(bias), _at(residual),
-            y.data_ptr(), _at(pre), _at(workspace), _size(workspace), status.data_ptr())
+            y.data_ptr(), _at(pre), _at(workspace), ws_bytes, status.data_ptr())
     return y, pre, status
 
 
@@ -876,6 +885,7 @@ def linear_bwd(dy, x, W, pre=None, activation=PRISM_ACT_NONE, dx=None, dW=None, 
     p = PrismLinearParams(M, K, N, in_heads, out_heads, int(activation), _code(dy.dtype, "dy"), PRISM_F32,
                           _code(dw_dtype, "dW"), xs, ws_, ys, N)
     _check_status(status)
+    ws_bytes = _size(workspace)
     lib = load()
     go = _Launch((dy, x, W, pre, dx, dW, db, workspace, status), stream)
     if dx is None and want_dx:
@@ -885,9 +895,10 @@ def linear_bwd(dy, x, W, pre=None, activation=PRISM_ACT_NONE, dx=None, dW=None, 
     if db is None and want_db:
         db = go.empty((N,), torch.float32)
     if workspace is None:
-        workspace = go.empty((max(int(lib.prism_linear_bwd_workspace_bytes(C.byref(p))), 16),), torch.uint8)
+        ws_bytes = max(int(lib.prism_linear_bwd_workspace_bytes(C.byref(p))), 16)
+        workspace = go.empty((ws_bytes,), torch.uint8)
     if status is None:
         status = go.zero_status()
     go.call("prism_linear_bwd", lib.prism_linear_bwd, C.byref(p), dy.data_ptr(), x.data_ptr(), W.data_ptr(), _at(pre),
-            _at(dx), _at(dW), _at(db), _at(workspace), _size(workspace), status.data_ptr())
+            _at(dx), _at(dW), _at(db), _at(workspace), ws_bytes, status.data_ptr())
     return dx, dW, db, status

@@ -124,3 +124,14 @@ def test_linear_gradients(lib):
         for a in _ends(at, size // 16 * 16, 16):
             assert call(st=a) == INV
     assert call(ws=DX + M_ * K_ * 2, st=DW - 16) == ok
+
+
+def test_binding_refuses_a_workspace_that_is_not_its_bytes():
+    """A strided or expanded workspace has fewer bytes in one piece than its elements say."""
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype)
+    x, w, q = z(10, 64), z(96, 64), z(2, 24, 64)
+    for ws in (z(1, dtype=torch.uint8).expand(1 << 20), z(1 << 20, dtype=torch.uint8)[::2], z(64, 64).t()[:32]):
+        for call in (lambda: _lib.linear(x, w, workspace=ws), lambda: _lib.linear_bwd(z(10, 96), x, w, workspace=ws),
+                     lambda: _lib.qk_norm_rope_bwd(q, None, q, workspace=ws)):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
