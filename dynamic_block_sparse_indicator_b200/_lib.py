@@ -622,6 +622,10 @@ class Rope:
     """A rotation table on the device with the grid and channels it belongs to (make_rope)."""
 
     def __init__(self, table, T, H, W, dims, pairing):
+        import torch
+        n = T * dims[0] + H * dims[1] + W * dims[2]
+        if table.dtype != torch.float32 or not table.is_contiguous() or table.numel() < n:
+            raise ValueError(f"the table must be {n} consecutive fp32")
         self.table, self.T, self.H, self.W, self.dims, self.pairing = table, T, H, W, tuple(dims), pairing
 
     def __repr__(self):

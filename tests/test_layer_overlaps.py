@@ -135,3 +135,12 @@ def test_binding_refuses_a_workspace_that_is_not_its_bytes():
                      lambda: _lib.qk_norm_rope_bwd(q, None, q, workspace=ws)):
             with pytest.raises(ValueError, match="workspace"):
                 call()
+
+
+def test_rope_refuses_a_table_that_is_not_its_grids():
+    """The kernels read T dim_t + H dim_h + W dim_w consecutive fp32 of it."""
+    good = torch.zeros(2 * 16 + 3 * 8 + 4 * 8)
+    _lib.Rope(good, 2, 3, 4, (16, 8, 8), 0)
+    for table in (good[:-1], good.double(), torch.zeros(1).expand(good.numel()), torch.zeros(2 * good.numel())[::2]):
+        with pytest.raises(ValueError, match="table"):
+            _lib.Rope(table, 2, 3, 4, (16, 8, 8), 0)
