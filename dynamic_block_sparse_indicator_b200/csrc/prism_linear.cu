@@ -1581,10 +1581,13 @@ static bool bad_params(const prism_linear_params* p) {
     if (p->activation < PRISM_ACT_NONE || p->activation > PRISM_ACT_SILU) return true;
     for (int d : {p->out_dtype, p->bias_dtype, p->dw_dtype})
         if (d != PRISM_BF16 && d != PRISM_F32) return true;
-    const int64_t most = 1LL << 38;        // a tensor map's stride is below 2^40 bytes
+    // a tensor map's stride is below 2^40 bytes: a tensor's rows (M, of W and dW N) times its stride,
+    // dx and dW (no wider than x and W) among them
+    const int64_t most = 1LL << 38;
     if (p->x_stride < p->K || p->w_stride < p->K || p->y_stride < p->N || p->r_stride < p->N) return true;
-    for (int64_t t : {p->x_stride, p->w_stride, p->y_stride, p->r_stride})
-        if (t > most / (p->M > p->N ? p->M + 1 : p->N + 1)) return true;
+    for (int64_t t : {p->x_stride, p->y_stride, p->r_stride})
+        if (t > most / (p->M + 1)) return true;
+    if (p->w_stride > most / ((int64_t)p->N + 1)) return true;
     if ((p->in_heads && p->x_stride != p->K) || (p->out_heads && (p->y_stride != p->N || p->r_stride != p->N)))
         return true;
     return false;

@@ -508,7 +508,8 @@ PRISM_API int prism_qk_norm_rope_bwd(const prism_norm_rope_params* p, const pris
  *   dw_dtype   of dW: PRISM_BF16 or PRISM_F32 each.
  *   x_stride, w_stride, y_stride, r_stride   elements between the rows of x, W
  *              ([N][K]), y or dy, residual; the contiguous count (K, K, N, N)
- *              where the tensor is head-major.
+ *              where the tensor is head-major.  A tensor's rows plus one times
+ *              its stride are at most 2^38 elements.
  * Arguments (device, 16-byte aligned)
  *   x, W       bf16.
  *   bias       [N] or NULL.  residual, in y's layout, or NULL; may be y itself.
