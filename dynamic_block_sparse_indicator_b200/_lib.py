@@ -866,7 +866,8 @@ def linear_bwd(dy, x, W, pre=None, activation=PRISM_ACT_NONE, dx=None, dW=None, 
                want_db=True, dw_dtype=None, workspace=None, status=None, stream=None):
     """(dx, dW, db, status): the gradients of linear by x (bf16, in x's layout), W ([N, K] of dw_dtype,
     fp32 if not given) and bias (fp32 [N]), each where wanted, from dy (in y's layout), the forward's x
-    and W, and with an activation its `pre`.  The residual's gradient is dy."""
+    and W, and with an activation its `pre`.  The residual's gradient is dy.  An fp32 dW through an
+    activation or from an fp32 dy takes two products; a bf16 one holds dz rounded to bf16 and takes one."""
     import torch
     M, K, in_heads, xs = _features(x, "x", torch.bfloat16)
     N, WK, wh, ws_ = _features(W, "W", torch.bfloat16)
@@ -886,8 +887,10 @@ def linear_bwd(dy, x, W, pre=None, activation=PRISM_ACT_NONE, dx=None, dW=None, 
                                   (db, (N,), torch.float32, "db")):
         if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous()):
             raise ValueError(f"{what} must be a contiguous {dtype} {shape}")
-    p = PrismLinearParams(M, K, N, in_heads, out_heads, int(activation), _code(dy.dtype, "dy"), PRISM_F32,
-                          _code(dw_dtype, "dW"), xs, ws_, ys, N)
+    # (an fp32 dW may take a second part of dz in the workspace: not where none is wanted)
+    dw_code = _code(dw_dtype, "dW") if want_dw or dW is not None else PRISM_BF16
+    p = PrismLinearParams(M, K, N, in_heads, out_heads, int(activation), _code(dy.dtype, "dy"), PRISM_F32, dw_code, xs, ws_,
+                          ys, N)
     _check_status(status)
     ws_bytes = _size(workspace)
     lib = load()

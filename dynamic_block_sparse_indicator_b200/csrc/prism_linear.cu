@@ -1257,6 +1257,7 @@ struct DzArgs {
     int64_t M, dy_total, pre_total;        // elements of the tensors
     int N, act;
     __nv_bfloat16* dz;                     // [M][dzs], or null (dy itself feeds the products)
+    __nv_bfloat16* lo;                     // [M][dzs], what dz's rounding leaves, or null
     int64_t dzs;
     float* part;                           // [row chunks][N] column sums, or null
     int64_t rows;                          // rows of a chunk
@@ -1304,11 +1305,17 @@ template <> struct Raw8<false, true> {
     }
 };
 
-// dz = dy act'(z) rounded to the products' 16 bits, and its column sums (of the unrounded
-// values): a block takes 256 columns of a chunk of rows, 8 rows at a time and U of those loaded
+// What a bf16 of the pair u leaves of (a, b), as bf16 itself (0 where it is not finite).
+__device__ __forceinline__ uint32_t left_bf16(uint32_t u, float a, float b) {
+    const float x = __uint_as_float(u << 16), y = __uint_as_float(u & 0xffff0000u);
+    return pack_bf16(fabsf(x) < INFINITY ? a - x : 0.f, fabsf(y) < INFINITY ? b - y : 0.f);
+}
+
+// dz = dy act'(z) rounded to the products' 16 bits (and, for an fp32 dW, what that rounding left, in
+// 16 bits again: together 2^-18 of it is lost), and its column sums (of the unrounded values): a block takes 256 columns of a chunk of rows, 8 rows at a time and U of those loaded
 // ahead, and adds its sums in a fixed order.  HBM-bound: one read of dy (and z), one write of dz.
-template <bool VEC, bool F32, int ACT>
-__global__ void __launch_bounds__(256, 4) k_dz(const DzArgs a) {
+template <bool VEC, bool F32, int ACT, bool LO>
+__global__ void __launch_bounds__(256, LO ? 3 : 4) k_dz(const DzArgs a) {
     constexpr int U = ACT ? 2 : 4;             // rows loaded ahead
     __shared__ float sm[8][256 + 8];
     const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
@@ -1326,9 +1333,14 @@ __global__ void __launch_bounds__(256, 4) k_dz(const DzArgs a) {
             }
             #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] += g[e];
-            if (a.dz)      // (the padding behind N is zero)
-                *reinterpret_cast<uint4*>(a.dz + r * a.dzs + c) =
-                    make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7]));
+            if (a.dz) {    // (the padding behind N is zero)
+                const uint4 u = make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7]));
+                *reinterpret_cast<uint4*>(a.dz + r * a.dzs + c) = u;
+                if (LO)
+                    *reinterpret_cast<uint4*>(a.lo + r * a.dzs + c) =
+                        make_uint4(left_bf16(u.x, g[0], g[1]), left_bf16(u.y, g[2], g[3]), left_bf16(u.z, g[4], g[5]),
+                                   left_bf16(u.w, g[6], g[7]));
+            }
         };
         int64_t r = (int64_t)blockIdx.y * a.rows + rl;
         if (c + 8 <= a.N)
@@ -1604,6 +1616,13 @@ static bool forms_dz(const prism_linear_params* p) {
     return p->activation != PRISM_ACT_NONE || p->out_dtype == PRISM_F32 || (!p->out_heads && p->y_stride % 8);
 }
 static size_t dz_bytes(const prism_linear_params* p) { return forms_dz(p) ? up256((size_t)p->M * pad8(p->N) * 2) : 0; }
+// whether dW is the sum of two products: an fp32 dW from a dz that has more than 16 bits.  One bf16 part
+// alone leaves 1.7e-3 of it, two leave 3e-6 (the sums' own truncation 7e-7); dx and a bf16 dW hold no
+// more than 16 bits themselves and take one.
+static bool two_parts(const prism_linear_params* p) {
+    return p->dw_dtype == PRISM_F32 && (p->activation != PRISM_ACT_NONE || p->out_dtype == PRISM_F32);
+}
+static size_t lo_bytes(const prism_linear_params* p) { return two_parts(p) ? dz_bytes(p) : 0; }
 
 struct DzGrid {
     int x, y;
@@ -1703,13 +1722,23 @@ static int forward(const prism_linear_params* p, const void* x, const void* W, c
     return product(mx, false, mw, false, p->M, p->N, p->K, a, s);
 }
 
+template <bool VEC, bool F32, int ACT>
+static void launch_dz_act(const DzArgs& d, dim3 grid, cudaStream_t s) {
+    if constexpr (F32 || ACT != PRISM_ACT_NONE) {
+        if (d.lo) {
+            k_dz<VEC, F32, ACT, true><<<grid, 256, 0, s>>>(d);
+            return;
+        }
+    }
+    k_dz<VEC, F32, ACT, false><<<grid, 256, 0, s>>>(d);
+}
 template <bool VEC, bool F32>
 static void launch_dz_of(const DzArgs& d, dim3 grid, cudaStream_t s) {
     switch (d.pre.p ? d.act : PRISM_ACT_NONE) {
-        case PRISM_ACT_GELU: k_dz<VEC, F32, PRISM_ACT_GELU><<<grid, 256, 0, s>>>(d); break;
-        case PRISM_ACT_GELU_TANH: k_dz<VEC, F32, PRISM_ACT_GELU_TANH><<<grid, 256, 0, s>>>(d); break;
-        case PRISM_ACT_SILU: k_dz<VEC, F32, PRISM_ACT_SILU><<<grid, 256, 0, s>>>(d); break;
-        default: k_dz<VEC, F32, PRISM_ACT_NONE><<<grid, 256, 0, s>>>(d); break;
+        case PRISM_ACT_GELU: launch_dz_act<VEC, F32, PRISM_ACT_GELU>(d, grid, s); break;
+        case PRISM_ACT_GELU_TANH: launch_dz_act<VEC, F32, PRISM_ACT_GELU_TANH>(d, grid, s); break;
+        case PRISM_ACT_SILU: launch_dz_act<VEC, F32, PRISM_ACT_SILU>(d, grid, s); break;
+        default: launch_dz_act<VEC, F32, PRISM_ACT_NONE>(d, grid, s); break;
     }
 }
 static void launch_dz(const DzArgs& d, dim3 grid, cudaStream_t s) {
@@ -1720,7 +1749,7 @@ static void launch_dz(const DzArgs& d, dim3 grid, cudaStream_t s) {
 
 static int backward(const prism_linear_params* p, const void* dy, const void* x, const void* W, const void* pre, void* dx,
                     void* dW, float* db, char* ws, int* err, cudaStream_t s) {
-    Matrix mx{}, mw{}, mz = matrix(dy, p->M, p->N, p->out_heads, p->y_stride);
+    Matrix mx{}, mw{}, mlo{}, mz = matrix(dy, p->M, p->N, p->out_heads, p->y_stride);
     int st = PRISM_OK;
     const bool dz = forms_dz(p) && (dx || dW);
     if (dz || db) {
@@ -1736,6 +1765,11 @@ static int backward(const prism_linear_params* p, const void* dy, const void* x,
             mz = Matrix{d.dz, p->M, p->N, d.dzs, 1};
         }
         ws += dz_bytes(p);
+        if (dW && two_parts(p)) {
+            d.lo = reinterpret_cast<__nv_bfloat16*>(ws);
+            mlo = Matrix{d.lo, p->M, p->N, d.dzs, 1};
+        }
+        ws += lo_bytes(p);
         const DzGrid g = dz_grid(p);
         d.rows = g.rows;
         if (db) d.part = reinterpret_cast<float*>(ws);
@@ -1761,6 +1795,11 @@ static int backward(const prism_linear_params* p, const void* dy, const void* x,
         Args a{};
         a.y = out_rows(dW, p->N, p->K, 0, p->K, p->dw_dtype == PRISM_F32);
         a.err = err;
+        if (mlo.p) {         // the small part first, the other added onto it
+            st = product(mlo, true, mx, true, p->N, p->K, p->M, a, s);
+            if (st) return st;
+            a.res = a.y;
+        }
         st = product(mz, true, mx, true, p->N, p->K, p->M, a, s);
     }
     return st;
@@ -1812,7 +1851,7 @@ extern "C" int prism_linear(const prism_linear_params* p, const void* x, const v
 extern "C" size_t prism_linear_bwd_workspace_bytes(const prism_linear_params* p) {
     using namespace prism::lin;
     if (bad_params(p)) return 0;
-    return x_bytes(p) + w_bytes(p) + dz_bytes(p) + up256((size_t)dz_grid(p).y * p->N * 4) + 256;
+    return x_bytes(p) + w_bytes(p) + dz_bytes(p) + lo_bytes(p) + up256((size_t)dz_grid(p).y * p->N * 4) + 256;
 }
 
 extern "C" int prism_linear_bwd(const prism_linear_params* p, const void* dy, const void* x, const void* W,
