@@ -927,6 +927,14 @@ struct Residual {
         }
         ++issued;
     }
+    // into L2 (columns outside C: nothing)
+    __device__ __forceinline__ void prefetch(const Args& a, int64_t r0, int c, int lane) {
+        if (lane == 0 && c < a.C) {
+            const int zh = a.res.hd ? c / a.res.hd : 0;
+            asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];"
+                         :: "l"(reinterpret_cast<uint64_t>(tm)), "r"(c - zh * a.res.hd), "r"((int)r0), "r"(zh) : "memory");
+        }
+    }
     __device__ __forceinline__ bool wait(const Args& a) {
         const bool ok = warp_wait(bar, waited & 1, a.err, 3302);
         waited += ok;
@@ -941,14 +949,21 @@ struct Residual {
     }
 };
 
+__device__ __forceinline__ float bias_at(const Args& a, int c) {
+    if (c >= a.C) return 0.f;
+    return a.bias_f32 ? __ldg(static_cast<const float*>(a.bias) + c)
+                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[c]);
+}
+
 // Lanes are rows of C.  Grid: pairs (CG 2) walk the tiles; or a cluster of `split` CTAs per tile.
 // Four epilogues for pairs, so that each keeps its registers, and one that has all for single CTAs:
 //   kSingle  one chunk, rows at 16-byte alignment: straight from the accumulator's columns.
-//   kDirect  several chunks, no activation, no kept z, the same alignment.  The registers' sums
-//            start from bias and residual, read while the first chunk runs, and leave from the
-//            registers, and the last accumulator is handed back as soon as it is added: with the
-//            residual read after the last chunk that held its accumulator longer than the next
-//            chunk lasted (783 cycles per stage instead of 563 with an fp32 residual).
+//   kDirect  several chunks, no activation, no kept z, the same alignment.  The registers' sums leave
+//            from the registers, and the last accumulator is handed back as soon as it is added; only
+//            then come bias and residual, whose first piece is in the stage since before the chunks and
+//            whose second takes the first's place.  (Sums that started from the residual were rounded
+//            at its size every chunk, and took longer: 92,160 x 5,120 x 5,120 of zeros with an fp32
+//            residual 2.75 ms, 2.70 now; 9,472 x 800 x 5,120 100 us, 93 now.)
 //   kSums    several chunks, the same alignment: their sum goes back to the last one's columns and
 //            leaves from there like a single chunk's.
 //   kRows    rows of any alignment.
@@ -1002,50 +1017,54 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
             const int64_t r0 = (int64_t)tr * F::kM + (CG == 2 ? 128 * (int)w.rank : 0) + q * 32;
             const int c0 = tc * BN + half * H;
             int buf = ac & 1;
-            if (MODE == kSingle && a.res.p && !a.pre.p && c0 < a.C) {                      // while the products run
+            if ((DIRECT || (MODE == kSingle && !a.pre.p)) && a.res.p && c0 < a.C) {        // while the products run
                 stage_free();
                 res.issue(a, r0, c0, lane);
+                // (the second piece's latency shows behind a block's last tile only: 2,600 x 5,000 x 2,000 67 us,
+                // 72 without; asked for at every tile it cost 92,160 x 5,120 x 5,120 3%)
+                if (DIRECT && a.y.f32 && t + w.step >= w.ntiles) res.prefetch(a, r0, c0 + 32, lane);
             }
             if (DIRECT || (MODE != kSingle && (w.nch > 1 || parts))) {
                 // the chunks add up in registers
                 float v[H];
-                if (DIRECT) {
-                    #pragma unroll
-                    for (int e = 0; e < H; ++e) v[e] = 0.f;
-                    #pragma unroll
-                    for (int e = 0; e < H; e += 32)
-                        if (a.res.p && ok && c0 + e < a.C) {
-                            if (e == 0) stage_free();
-                            if (e == 0 || a.y.f32) {
-                                res.issue(a, r0, c0 + e, lane);
-                                ok = res.wait(a);
-                            }
-                            if (ok) add_own(a.y.f32, stage, lane, a.y.f32 ? 0 : e, v + e);
-                        }
-                    if (!ok) break;
-                    #pragma unroll
-                    for (int e = 0; e < H; e += 8) {
-                        const int n = min(8, a.C - (c0 + e));
-                        if (n > 0) finish<8, false, false>(a, v + e, r0 + lane, c0 + e, n);
-                    }
-                }
                 for (int ch = 0; ch < w.nch; ++ch, ++ac) {
                     buf = ac & 1;
                     if (!warp_wait(&sm.acc_full[buf], (ac / 2) & 1, a.err, 3301)) { ok = false; break; }
                     tc_fence_after();
-                    add_columns<H>(at0 + buf * BN, v, ch == 0 && !DIRECT);
+                    add_columns<H>(at0 + buf * BN, v, ch == 0);
                     if (DIRECT || ch < w.nch - 1) release<CG>(sm, buf, lane);
                 }
                 if (!ok) break;
                 if (DIRECT) {
-                    if (c0 < a.C) {
-                        stage_free();
-                        put_own(a.y.f32, stage, lane, 0, v);
-                        if (!a.y.f32) put_bf16(stage, lane, 32, v + 32);
-                        leave(c0, r0);
+                    // (the tile's place is worked out again: held over the chunks it cost spilled registers)
+                    int u = t, uc, ur;
+                    asm volatile("" : "+r"(u));
+                    tile_at(a, u, uc, ur);
+                    const int c0 = uc * BN + half * H;
+                    const int64_t r0 = (int64_t)ur * F::kM + (CG == 2 ? 128 * (int)w.rank : 0) + q * 32;
+                    if (c0 >= a.C) continue;
+                    if (a.bias) {                              // a column's bias in its lane
+                        const float b0 = bias_at(a, c0 + lane), b1 = bias_at(a, c0 + 32 + lane);
+                        #pragma unroll
+                        for (int e = 0; e < H; ++e) v[e] += __shfl_sync(0xffffffffu, e < 32 ? b0 : b1, e & 31);
                     }
+                    if (a.res.p) {
+                        if (!res.wait(a)) { ok = false; break; }
+                        add_own(a.y.f32, stage, lane, 0, v);
+                        if (!a.y.f32) add_own(false, stage, lane, 32, v + 32);
+                    } else {
+                        stage_free();
+                    }
+                    put_own(a.y.f32, stage, lane, 0, v);
+                    if (!a.y.f32) put_bf16(stage, lane, 32, v + 32);
+                    leave(c0, r0);
                     if (a.y.f32 && c0 + 32 < a.C) {
                         stage_free();
+                        if (a.res.p) {
+                            res.issue(a, r0, c0 + 32, lane);
+                            if (!res.wait(a)) { ok = false; break; }
+                            add_own(true, stage, lane, 0, v + 32);
+                        }
                         put_own(true, stage, lane, 0, v + 32);
                         leave(c0 + 32, r0);
                     }

@@ -79,3 +79,32 @@ def test_weight_gradient_of_values_that_are_not_finite(cuda_device):
     keep = torch.ones(96, dtype=torch.bool, device="cuda")
     keep[5] = keep[7] = False
     assert torch.equal(dW[keep], clean[keep])
+
+
+# M, K, N: k_few whole and split; single CTAs whole, split and of any alignment; pairs of one chunk, of several (768 and
+# 16,384 elements), ragged, with a column tile that is partly outside, and of any alignment
+RES_SHAPES = [(5, 640, 256), (13, 4224, 256), (60, 1280, 129), (100, 640, 136), (100, 5000, 136), (100, 900, 131),
+              (2571, 640, 2120), (2500, 5000, 2000), (2571, 1700, 2120), (600, 5000, 4160), (2560, 17000, 2056), (2571, 5000, 2121)]
+
+
+@pytest.mark.parametrize("M,K,N", RES_SHAPES)
+@pytest.mark.parametrize("heads", [False, True], ids=["rows", "heads"])
+@pytest.mark.parametrize("bias", [False, True], ids=["no_bias", "bias"])
+def test_a_large_residual_is_added_once(M, K, N, heads, bias, cuda_device):
+    """x W^T + b of integers below 2^24 is exact, so y is the residual plus it with one rounding, however
+    large the residual: 30,000 times a normal value, with all its fraction bits.  In place too."""
+    if heads:
+        N = -(-N // 64) * 64
+    g = _gen(K)
+    x, W = _ints(g, 3, M, K, dtype=BF), _ints(g, 3, N, K, dtype=BF)
+    b = _ints(g, 9, N) if bias else None
+    shape = (N // 64, M, 64) if heads else (M, N)
+    z = x.double() @ W.double().t() + (b.double() if bias else 0)
+    z = ref.heads(z, N // 64) if heads else z
+    r = torch.randn(shape, generator=g, device="cuda") * 3e4
+    want = (z + r.double()).float()
+    y, _, st = _lib.linear(x, W, b, r, out_heads=N // 64 if heads else 0)
+    assert torch.equal(y, want)
+    y, _, st = _lib.linear(x, W, b, r, y=r, status=st)
+    assert y is r and torch.equal(r, want)
+    assert _lib.status_read(st)[0] == _lib.PRISM_OK

@@ -48,8 +48,9 @@ def run(roles, counts, seed):
     return f"after the blocks' end: {sorted(set(flying))}" if flying else None
 
 
-def roles(cg, stages, epi, tiles, nk, chunk, drain=True):
-    """`drain` False leaves out the producers' last wait for the stages' `empty` barriers."""
+def roles(cg, stages, epi, tiles, nk, chunk, drain=True, pieces=0):
+    """`drain` False leaves out the producers' last wait for the stages' `empty` barriers.  `pieces`: a
+    tile's pieces of residual, the first asked for before the chunks, each waited for after them."""
     nch = -(-nk // chunk)
     sizes = [nk * (c + 1) // nch - nk * c // nch for c in range(nch)]
     total = tiles * nk
@@ -83,13 +84,20 @@ def roles(cg, stages, epi, tiles, nk, chunk, drain=True):
                     yield ("later", ("acc_full", cta, buf))
                 ac += 1
 
-    def warp(cta):
-        for ac in range(tiles * nch):
-            yield ("wait", ("acc_full", cta, ac & 1), ac // 2)
-            yield ("arrive", ("acc_empty", ac & 1))
+    def warp(cta, i):
+        for t in range(tiles):
+            if pieces:
+                yield ("later", ("res", cta, i))
+            for ac in range(t * nch, (t + 1) * nch):
+                yield ("wait", ("acc_full", cta, ac & 1), ac // 2)
+                yield ("arrive", ("acc_empty", ac & 1))
+            for k in range(pieces):
+                if k:
+                    yield ("later", ("res", cta, i))
+                yield ("wait", ("res", cta, i), t * pieces + k)
 
     rs = [issuer] + [(lambda c=c: producer(c)) for c in range(cg)]
-    rs += [(lambda c=c: warp(c)) for c in range(cg) for _ in range(epi)]
+    rs += [(lambda c=c, i=i: warp(c, i)) for c in range(cg) for i in range(epi)]
     counts = {("full", s): cg for s in range(stages)}
     counts.update({("acc_empty", b): epi * cg for b in range(2)})
     return rs, counts
@@ -100,9 +108,10 @@ SIZES = [(1, 1, 12), (1, 13, 4), (3, 1, 12), (4, 7, 3), (5, 12, 12), (2, 25, 12)
 
 @pytest.mark.parametrize("cg,stages,epi", [(1, 3, 2), (1, 6, 8), (2, 5, 2), (2, 6, 3)])
 @pytest.mark.parametrize("tiles,nk,chunk", SIZES)
-def test_nothing_arrives_after_the_end(cg, stages, epi, tiles, nk, chunk):
+@pytest.mark.parametrize("pieces", [0, 1, 2])
+def test_nothing_arrives_after_the_end(cg, stages, epi, tiles, nk, chunk, pieces):
     for seed in range(12):
-        assert run(*roles(cg, stages, epi, tiles, nk, chunk), seed) is None
+        assert run(*roles(cg, stages, epi, tiles, nk, chunk, pieces=pieces), seed) is None
 
 
 @pytest.mark.parametrize("cg,stages,epi", [(1, 6, 8), (2, 5, 2)])
