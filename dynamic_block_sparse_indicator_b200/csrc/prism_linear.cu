@@ -273,6 +273,8 @@ __device__ __forceinline__ void times_grad(float& g0, float& g1, float z0, float
         s0 = rcp(1.f + ex2(q0));
         s1 = rcp(1.f + ex2(q1));
         ffma2(q0, q1, a0, a1, 3.f * d, 3.f * d, c, c);       // t'
+        q0 = fminf(q0, 3e38f);                               // (s (1 - s) is 0 where z^2 overflows)
+        q1 = fminf(q1, 3e38f);
         ffma2(u0, u1, s0, s1, -1.f, -1.f, 1.f, 1.f);
         fmul2(w0, w1, z0, z1, s0, s1);
         fmul2(w0, w1, w0, w1, u0, u1);
