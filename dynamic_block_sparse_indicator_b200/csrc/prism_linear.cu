@@ -1247,9 +1247,9 @@ __device__ __forceinline__ void read8(const Out& o, int64_t off, int64_t r, int 
 }
 
 // Rows [rows][K] whose stride a TMA map cannot take (no multiple of 8 elements), copied to a
-// padded stride in the workspace (the padding is zero).
+// padded stride in the workspace (the padding is zero); and copied again to `dst2`, where given.
 __global__ void __launch_bounds__(256) k_pack(const __nv_bfloat16* src, int64_t stride, int64_t rows, int K,
-                                              __nv_bfloat16* dst, int groups) {
+                                              __nv_bfloat16* dst, __nv_bfloat16* dst2, int groups) {
     const int64_t total = (rows - 1) * stride + K;
     // a block takes one row's groups at a time, or several short rows
     const int per = groups < 256 ? 256 / groups : 1;
@@ -1270,6 +1270,7 @@ __global__ void __launch_bounds__(256) k_pack(const __nv_bfloat16* src, int64_t 
                 x = make_uint4(w[0], w[1], w[2], w[3]);
             }
             reinterpret_cast<uint4*>(dst)[r * groups + g] = x;
+            if (dst2) reinterpret_cast<uint4*>(dst2)[r * groups + g] = x;
         }
 }
 
@@ -1636,14 +1637,23 @@ static size_t w_bytes(const prism_linear_params* p) { return pack_w(p) ? up256((
 static bool forms_dz(const prism_linear_params* p) {
     return p->activation != PRISM_ACT_NONE || p->out_dtype == PRISM_F32 || (!p->out_heads && p->y_stride % 8);
 }
-static size_t dz_bytes(const prism_linear_params* p) { return forms_dz(p) ? up256((size_t)p->M * pad8(p->N) * 2) : 0; }
 // whether dW is the sum of two products: an fp32 dW from a dz that has more than 16 bits.  One bf16 part
 // alone leaves 1.7e-3 of it, two leave 3e-6 (the sums' own truncation 7e-7); dx and a bf16 dW hold no
 // more than 16 bits themselves and take one.
 static bool two_parts(const prism_linear_params* p) {
     return p->dw_dtype == PRISM_F32 && (p->activation != PRISM_ACT_NONE || p->out_dtype == PRISM_F32);
 }
-static size_t lo_bytes(const prism_linear_params* p) { return two_parts(p) ? dz_bytes(p) : 0; }
+// The parts lie one behind the other.  With fewer rows than features they are one contraction of 2 M
+// rows against x twice (x copied: dW, the largest tensor then, is written once; one token, 30,720 x 5,120
+// through SiLU with dx 212 us, as two products 419; 2,477 x 5,120 x 20,480 1,186 and 1,260), else two
+// products, the second added onto the first.
+static bool stacked(const prism_linear_params* p) { return two_parts(p) && !p->in_heads && p->M < p->N; }
+static size_t parts_bytes(const prism_linear_params* p) {
+    return forms_dz(p) ? up256((size_t)p->M * pad8(p->N) * (two_parts(p) ? 4 : 2)) : 0;
+}
+static size_t x_twice_bytes(const prism_linear_params* p) {
+    return stacked(p) ? up256((size_t)p->M * pad8(p->K) * 4) : x_bytes(p);
+}
 
 struct DzGrid {
     int x, y;
@@ -1707,21 +1717,21 @@ static int device_ok() {
     return major == 10 && minor == 0 ? PRISM_OK : PRISM_ERR_UNSUPPORTED;
 }
 
-// A matrix of rows as the products read it: itself, or packed at `ws`.
+// A matrix of rows as the products read it: itself, or packed at `ws` (`twice`: and once more behind it).
 static int operand(Matrix* m, const void* p, int64_t rows, int cols, int heads, int64_t stride, bool pack, char*& ws,
-                   cudaStream_t s) {
-    if (!pack) {
+                   cudaStream_t s, bool twice = false) {
+    if (!pack && !twice) {
         *m = matrix(p, rows, cols, heads, stride);
         return PRISM_OK;
     }
     const int64_t ld = pad8(cols);
     auto* dst = reinterpret_cast<__nv_bfloat16*>(ws);
-    ws += up256((size_t)rows * ld * 2);
+    ws += up256((size_t)rows * ld * (twice ? 4 : 2));
     const int groups = (int)(ld / 8), per = groups < 256 ? 256 / groups : 1;
     const int64_t blocks = ceil_div(rows, per);
     k_pack<<<(unsigned)(blocks < 148 * 32 ? blocks : 148 * 32), 256, 0, s>>>(static_cast<const __nv_bfloat16*>(p), stride, rows,
-                                                                            cols, dst, groups);
-    *m = Matrix{dst, rows, cols, ld, 1};
+                                                                            cols, dst, twice ? dst + rows * ld : nullptr, groups);
+    *m = Matrix{dst, twice ? 2 * rows : rows, cols, ld, 1};
     return cudaGetLastError() == cudaSuccess ? PRISM_OK : PRISM_ERR_CUDA;
 }
 
@@ -1785,12 +1795,11 @@ static int backward(const prism_linear_params* p, const void* dy, const void* x,
             d.dzs = pad8(p->N);
             mz = Matrix{d.dz, p->M, p->N, d.dzs, 1};
         }
-        ws += dz_bytes(p);
         if (dW && two_parts(p)) {
-            d.lo = reinterpret_cast<__nv_bfloat16*>(ws);
+            d.lo = d.dz + p->M * d.dzs;
             mlo = Matrix{d.lo, p->M, p->N, d.dzs, 1};
         }
-        ws += lo_bytes(p);
+        ws += parts_bytes(p);
         const DzGrid g = dz_grid(p);
         d.rows = g.rows;
         if (db) d.part = reinterpret_cast<float*>(ws);
@@ -1811,17 +1820,20 @@ static int backward(const prism_linear_params* p, const void* dy, const void* x,
         if (st) return st;
     }
     if (dW) {
-        st = operand(&mx, x, p->M, p->K, p->in_heads, p->x_stride, pack_x(p), ws, s);
+        const bool twice = stacked(p);
+        st = operand(&mx, x, p->M, p->K, p->in_heads, p->x_stride, pack_x(p), ws, s, twice);
         if (st) return st;
         Args a{};
         a.y = out_rows(dW, p->N, p->K, 0, p->K, p->dw_dtype == PRISM_F32);
         a.err = err;
-        if (mlo.p) {         // the small part first, the other added onto it
+        if (twice) {
+            mz.rows = 2 * p->M;
+        } else if (mlo.p) {  // the small part first, the other added onto it
             st = product(mlo, true, mx, true, p->N, p->K, p->M, a, s);
             if (st) return st;
             a.res = a.y;
         }
-        st = product(mz, true, mx, true, p->N, p->K, p->M, a, s);
+        st = product(mz, true, mx, true, p->N, p->K, mz.rows, a, s);
     }
     return st;
 }
@@ -1872,7 +1884,7 @@ extern "C" int prism_linear(const prism_linear_params* p, const void* x, const v
 extern "C" size_t prism_linear_bwd_workspace_bytes(const prism_linear_params* p) {
     using namespace prism::lin;
     if (bad_params(p)) return 0;
-    return x_bytes(p) + w_bytes(p) + dz_bytes(p) + lo_bytes(p) + up256((size_t)dz_grid(p).y * p->N * 4) + 256;
+    return x_twice_bytes(p) + w_bytes(p) + parts_bytes(p) + up256((size_t)dz_grid(p).y * p->N * 4) + 256;
 }
 
 extern "C" int prism_linear_bwd(const prism_linear_params* p, const void* dy, const void* x, const void* W,

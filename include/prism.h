@@ -552,7 +552,8 @@ PRISM_API int prism_linear(const prism_linear_params* p, const void* x, const vo
  *        activation and with a bf16 dy.  Otherwise dx and a bf16 dW take it
  *        rounded to nearest, and an fp32 dW is the sum of two products, of dz
  *        rounded and of what that left (2^-18 of dz is lost; the time of one
- *        product more).  db sums the unrounded values.
+ *        product more; an infinity in x gives NaN there).  db sums the unrounded
+ *        values.
  *   dx   bf16, contiguous in x's layout; dW [N][K] of dw_dtype, contiguous; db
  *        fp32 [N]: written, each NULL if not wanted (M = 0 writes zeros to dW
  *        and db).  W may be NULL without dx, x without dW.

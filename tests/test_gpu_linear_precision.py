@@ -43,6 +43,26 @@ def test_weight_gradient_keeps_fp32_dy(M, K, N, cuda_device):
     assert _lib.status_read(st)[0] == _lib.PRISM_OK
 
 
+@pytest.mark.parametrize("M,heads,D,N", [(1, 2, 64, 192), (50, 3, 128, 257), (700, 5, 64, 320), (1500, 10, 128, 2048)])
+@pytest.mark.parametrize("slices", [False, True], ids=["own", "slices"])
+def test_weight_gradient_keeps_fp32_dy_of_heads_and_slices(M, heads, D, N, slices, cuda_device):
+    """The same with x and dy head-major, and with both as columns of wider buffers of odd strides."""
+    g = _gen(M)
+    K, oh = heads * D, N // 64 if N % 64 == 0 else 0
+    dy, x = _ints(g, 1 << (15 if M <= 128 else 11), M, N), _ints(g, 3, M, K, dtype=BF)
+    want, W = (dy.double().t() @ x.double()).float(), _ints(g, 1, N, K, dtype=BF)
+    if slices:
+        hold = [torch.full((M, t.shape[1] + 5), 7.0, dtype=t.dtype, device="cuda") for t in (dy, x)]
+        for h, t in zip(hold, (dy, x)):
+            h[:, :t.shape[1]] = t
+        dy, x = hold[0][:, :N], hold[1][:, :K]
+    else:
+        dy, x = (ref.heads(t, n).contiguous() for t, n in ((dy, oh), (x, heads)))
+    dW, st = _lib.linear_bwd(dy, x, W, want_dx=False, want_db=False)[1::2]
+    assert torch.equal(dW, want)
+    assert _lib.status_read(st)[0] == _lib.PRISM_OK
+
+
 @pytest.mark.parametrize("act", [1, 2, 3])
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("M,K,N", DW_SHAPES)
