@@ -162,7 +162,7 @@ __device__ __forceinline__ void read_w(const float4* sw, int ch, float* w) {
 //              and the places of their partners.
 //   kLanes     halves of axes whose d / 2 is a multiple of 8: the partners of a lane's channels are
 //              the channels of one other lane, brought by shuffles of the loaded words (40 heads of
-//              92,160 tokens, bf16: forward 5.6 TB/s and backward 5.3, through shared memory 5.3 and 4.4).
+//              92,160 tokens, bf16: forward 5.7 TB/s and backward 5.3, through shared memory 5.2 and 4.6).
 // Channels behind the last axis are not rotated: cos 1, sin 0.
 constexpr int kAdjacent = 0, kHalves = 1, kLanes = 2;
 template <int PAIRS> struct Turn;
@@ -346,10 +346,11 @@ __device__ __forceinline__ void scale8(float* x, float r) {
 // The weights are folded into the rotation, y_a = r (x_a w_a c - x_b w_b s): the factors are made
 // once per token and tensor, and with halves the rows pass through shared memory as they were
 // read, so a group's exchange does not wait for its norms.  At 40 heads of 92,160 tokens adjacent
-// pairs move 6.3 TB/s (64 registers for 4 blocks per SM; 3 blocks 6.2, 6 blocks with U = 2 5.5) and
-// halves 5.3: there shared memory is 82% busy, eight words written and eight read per lane and row
-// (unfolded, every row summed by itself: 4.3).  At 5 heads, 1,013,760 tokens, 5.1: a token's factors
-// and addresses serve ten rows only.
+// pairs move 6.2 TB/s (64 registers for 4 blocks per SM; 3 blocks 6.2, 6 blocks with U = 2 5.5) and
+// halves 5.2: there shared memory is 82% busy, eight words written and eight read per lane and row
+// (unfolded, every row summed by itself: 4.3).  At 5 heads, 1,013,760 tokens, 5.0: a token's factors
+// and addresses serve ten rows only, and five heads are a group of four and one of a single row, for
+// each tensor, so 2.5 loads of 4 are in flight on average.
 template <typename TI, typename TO, int D, int PAIRS>
 __global__ void __launch_bounds__(kThreads, PAIRS == kAdjacent ? 4 : 3) k_norm_rope(const Args a) {
     constexpr int U = sizeof(TI) == 2 ? 4 : 2;
@@ -421,8 +422,8 @@ __global__ void __launch_bounds__(kThreads, PAIRS == kAdjacent ? 4 : 3) k_norm_r
 template <typename TI, typename TG, int D, int PAIRS>
 __global__ void __launch_bounds__(kThreads, 2) k_norm_rope_bwd(const Args a) {
     // rows at a time: four, but two where four rows' fp32 gradients and their exchange do not fit the
-    // registers (40 heads of 92,160 tokens, halves: fp32 5.0 TB/s with two and 4.0 with four, bf16 4.0
-    // and 4.6; adjacent 5.6 and 6.6, 3.6 and 5.4)
+    // registers (40 heads of 92,160 tokens, halves: fp32 4.7 TB/s with two and 4.0 with four, bf16 4.0
+    // and 4.6; adjacent 5.6 and 6.4, 3.6 and 5.5)
     constexpr int U = PAIRS == kHalves && sizeof(TG) == 4 ? 2 : 4;
     constexpr bool HALVES = PAIRS == kHalves, KEEP = PAIRS != kAdjacent;
     using G = Group<TG, D, PAIRS, U>;
