@@ -913,10 +913,9 @@ __device__ __forceinline__ void put_own(bool f32, uint32_t stage, int lane, int 
 struct Residual {
     const void* tm;
     uint64_t* bar;
-    uint32_t stage;
     int issued = 0, waited = 0;
-    // the stage must be free; every lane's accesses to it come first
-    __device__ __forceinline__ void issue(const Args& a, int64_t r0, int c, int lane) {
+    // to 4 KB that must be free; every lane's accesses to them come first
+    __device__ __forceinline__ void issue(const Args& a, uint32_t to, int64_t r0, int c, int lane) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -924,18 +923,10 @@ struct Residual {
             mbar_expect_tx(bar, 4096);
             asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
                          " [%0], [%1, {%3, %4, %5}], [%2];"
-                         :: "r"(stage), "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(c - zh * a.res.hd),
+                         :: "r"(to), "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(c - zh * a.res.hd),
                             "r"((int)r0), "r"(zh) : "memory");
         }
         ++issued;
-    }
-    // into L2 (columns outside C: nothing)
-    __device__ __forceinline__ void prefetch(const Args& a, int64_t r0, int c, int lane) {
-        if (lane == 0 && c < a.C) {
-            const int zh = a.res.hd ? c / a.res.hd : 0;
-            asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];"
-                         :: "l"(reinterpret_cast<uint64_t>(tm)), "r"(c - zh * a.res.hd), "r"((int)r0), "r"(zh) : "memory");
-        }
     }
     __device__ __forceinline__ bool wait(const Args& a) {
         const bool ok = warp_wait(bar, waited & 1, a.err, 3302);
@@ -963,9 +954,11 @@ __device__ __forceinline__ float bias_at(const Args& a, int c) {
 //   kDirect  several chunks, no activation, no kept z, the same alignment.  The registers' sums leave
 //            from the registers, and the last accumulator is handed back as soon as it is added; only
 //            then come bias and residual, whose first piece is in the stage since before the chunks and
-//            whose second takes the first's place.  (Sums that started from the residual were rounded
-//            at its size every chunk, and took longer: 92,160 x 5,120 x 5,120 of zeros with an fp32
-//            residual 2.75 ms, 2.70 now; 9,472 x 800 x 5,120 100 us, 93 now.)
+//            whose second takes the first's place (behind a block's last product, where nothing else
+//            runs, a place in the ring: 2,600 x 5,000 x 2,000 65 us, 67 in the first's place).  Sums that
+//            started from the residual were rounded at its size every chunk, and took longer: 92,160 x
+//            5,120 x 5,120 of zeros with an fp32 residual 2.75 ms, 2.69 now; 9,472 x 800 x 5,120 100 us,
+//            92 now.
 //   kSums    several chunks, the same alignment: their sum goes back to the last one's columns and
 //            leaves from there like a single chunk's.
 //   kRows    rows of any alignment.
@@ -997,13 +990,13 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
         const bool parts = CG == 1 && a.split > 1;
         int ac = 0;
         bool ok = true;
-        // the stage's 32 rows from column c on leave; what lies outside C is not written
-        auto leave = [&](int c, int64_t r0) {
+        // the 32 rows at `from`, from column c on, leave; what lies outside C is not written
+        auto leave = [&](uint32_t from, int c, int64_t r0) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 const int zh = a.y.hd ? c / a.y.hd : 0;
-                tma_store_3d(&tm_y, stage, c - zh * a.y.hd, (int)r0, zh);
+                tma_store_3d(&tm_y, from, c - zh * a.y.hd, (int)r0, zh);
                 bulk_commit();
             }
         };
@@ -1012,7 +1005,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
             __syncwarp();
         };
         const int piece = a.y.f32 ? 32 : 64;                   // columns of a stage's row
-        Residual res{&tm_r, &res_full[warp], stage};
+        Residual res{&tm_r, &res_full[warp]};
         for (int t = w.first; ok && t < w.ntiles; t += w.step) {
             int tc, tr;
             tile_at(a, t, tc, tr);
@@ -1021,16 +1014,19 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
             int buf = ac & 1;
             if ((DIRECT || (MODE == kSingle && !a.pre.p)) && a.res.p && c0 < a.C) {        // while the products run
                 stage_free();
-                res.issue(a, r0, c0, lane);
-                // (the second piece's latency shows behind a block's last tile only: 2,600 x 5,000 x 2,000 67 us,
-                // 72 without; asked for at every tile it cost 92,160 x 5,120 x 5,120 3%)
-                if (DIRECT && a.y.f32 && t + w.step >= w.ntiles) res.prefetch(a, r0, c0 + 32, lane);
+                res.issue(a, stage, r0, c0, lane);
             }
             if (DIRECT || (MODE != kSingle && (w.nch > 1 || parts))) {
                 // the chunks add up in registers
-                float v[H];
+                float v[H], b0 = 0.f, b1 = 0.f;
+                const bool last = t + w.step >= w.ntiles;
+                auto take_bias = [&]() {                       // a column's bias in its lane
+                    b0 = bias_at(a, c0 + lane);
+                    b1 = bias_at(a, c0 + 32 + lane);
+                };
                 for (int ch = 0; ch < w.nch; ++ch, ++ac) {
                     buf = ac & 1;
+                    if (DIRECT && a.bias && last && ch == w.nch - 1) take_bias();
                     if (!warp_wait(&sm.acc_full[buf], (ac / 2) & 1, a.err, 3301)) { ok = false; break; }
                     tc_fence_after();
                     add_columns<H>(at0 + buf * BN, v, ch == 0);
@@ -1038,37 +1034,37 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                 }
                 if (!ok) break;
                 if (DIRECT) {
-                    // (the tile's place is worked out again: held over the chunks it cost spilled registers)
-                    int u = t, uc, ur;
-                    asm volatile("" : "+r"(u));
-                    tile_at(a, u, uc, ur);
-                    const int c0 = uc * BN + half * H;
-                    const int64_t r0 = (int64_t)ur * F::kM + (CG == 2 ? 128 * (int)w.rank : 0) + q * 32;
                     if (c0 >= a.C) continue;
-                    if (a.bias) {                              // a column's bias in its lane
-                        const float b0 = bias_at(a, c0 + lane), b1 = bias_at(a, c0 + 32 + lane);
+                    // behind a block's last product the ring is free, and a second piece has a place of its own there
+                    const bool two = a.y.f32 && c0 + 32 < a.C;
+                    const uint32_t second = last ? ring + warp * kStageOut : stage;
+                    if (a.res.p) {
+                        if (!res.wait(a)) { ok = false; break; }
+                        if (two && last) res.issue(a, second, r0, c0 + 32, lane);
+                    } else {
+                        stage_free();
+                    }
+                    if (a.bias) {
+                        if (!last) take_bias();
                         #pragma unroll
                         for (int e = 0; e < H; ++e) v[e] += __shfl_sync(0xffffffffu, e < 32 ? b0 : b1, e & 31);
                     }
                     if (a.res.p) {
-                        if (!res.wait(a)) { ok = false; break; }
                         add_own(a.y.f32, stage, lane, 0, v);
                         if (!a.y.f32) add_own(false, stage, lane, 32, v + 32);
-                    } else {
-                        stage_free();
                     }
                     put_own(a.y.f32, stage, lane, 0, v);
                     if (!a.y.f32) put_bf16(stage, lane, 32, v + 32);
-                    leave(c0, r0);
-                    if (a.y.f32 && c0 + 32 < a.C) {
-                        stage_free();
+                    leave(stage, c0, r0);
+                    if (two) {
+                        if (!last) stage_free();
                         if (a.res.p) {
-                            res.issue(a, r0, c0 + 32, lane);
+                            if (!last) res.issue(a, second, r0, c0 + 32, lane);
                             if (!res.wait(a)) { ok = false; break; }
-                            add_own(true, stage, lane, 0, v + 32);
+                            add_own(true, second, lane, 0, v + 32);
                         }
-                        put_own(true, stage, lane, 0, v + 32);
-                        leave(c0 + 32, r0);
+                        put_own(true, second, lane, 0, v + 32);
+                        leave(second, c0 + 32, r0);
                     }
                     continue;
                 }
@@ -1118,7 +1114,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                         __syncwarp();
                     }
                     if (a.res.p) {
-                        if (res.issued == res.waited) res.issue(a, r0, c, lane);
+                        if (res.issued == res.waited) res.issue(a, stage, r0, c, lane);
                         if (!res.wait(a)) { ok = false; break; }
                     }
                     #pragma unroll 1
@@ -1132,7 +1128,7 @@ k_tile(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtenso
                         if (a.res.p) add_own(a.y.f32, stage, lane, k, z);
                         put_own(a.y.f32, stage, lane, k, z);
                     }
-                    leave(c, r0);
+                    leave(stage, c, r0);
                 }
             } else {
                 // rows at any alignment: turned in the stage, so that a row's columns lie in the lanes
@@ -1334,7 +1330,8 @@ __device__ __forceinline__ uint32_t left_bf16(uint32_t u, float a, float b) {
 }
 
 // dz = dy act'(z) rounded to the products' 16 bits (and, for an fp32 dW, what that rounding left, in
-// 16 bits again: together 2^-18 of it is lost), and its column sums (of the unrounded values): a block takes 256 columns of a chunk of rows, 8 rows at a time and U of those loaded
+// 16 bits again: together 2^-18 of it is lost), and its column sums (of the unrounded values): a block
+// takes 256 columns of a chunk of rows, 8 rows at a time and U of those loaded
 // ahead, and adds its sums in a fixed order.  HBM-bound: one read of dy (and z), one write of dz.
 template <bool VEC, bool F32, int ACT, bool LO>
 __global__ void __launch_bounds__(256, LO ? 3 : 4) k_dz(const DzArgs a) {
@@ -1638,7 +1635,7 @@ static bool forms_dz(const prism_linear_params* p) {
     return p->activation != PRISM_ACT_NONE || p->out_dtype == PRISM_F32 || (!p->out_heads && p->y_stride % 8);
 }
 // whether dW is the sum of two products: an fp32 dW from a dz that has more than 16 bits.  One bf16 part
-// alone leaves 1.7e-3 of it, two leave 3e-6 (the sums' own truncation 7e-7); dx and a bf16 dW hold no
+// alone leaves 1.7e-3 of it, two leave 2.6e-6 (the sums' own truncation 7e-7); dx and a bf16 dW hold no
 // more than 16 bits themselves and take one.
 static bool two_parts(const prism_linear_params* p) {
     return p->dw_dtype == PRISM_F32 && (p->activation != PRISM_ACT_NONE || p->out_dtype == PRISM_F32);

@@ -399,7 +399,8 @@ PRISM_API int prism_status_read(int32_t* dev_status, int32_t* site, void* stream
  *   square, multiplied by a weight and rotated by the token's grid position,
  *     u = x w / sqrt(mean_d x_d^2 + eps),
  *     y_a = u_a cos - u_b sin,  y_b = u_a sin + u_b cos  for each pair (a, b),
- *   in one pass (fp32 arithmetic, one rounding to out_dtype).
+ *   in one pass (fp32 arithmetic, one rounding to out_dtype; the squares of a
+ *   row sum in fp32, so values near 1e19 and above give zeros).
  * prism_norm_rope_params
  *   N          tokens, 0 .. 2^31 - 1 (0: the call does nothing).
  *   T, H, W    the grid, T H W = N, token n = (t H + h) W + w; any positive
